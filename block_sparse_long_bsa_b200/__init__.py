@@ -1,5 +1,6 @@
 """Python binding of ``libbsa.so``: block-sparse causal attention on B200
-(forward, gradients, selected-page decode).
+(forward, gradients, selected-page decode, attention of drafted token trees and
+cache eviction by attention weight).
 
 Argument marshalling only.  Every step of the computation runs in the
 library's CUDA kernel or its host layout compiler; this module converts Python
@@ -10,9 +11,11 @@ shared library is missing or cannot be loaded, every call raises.
 Names follow the C ABI: ``bsa_build_layout``, ``bsa_layout_csr``,
 ``bsa_layout_csc``, ``bsa_layout_order``, ``bsa_layout_segments``,
 ``bsa_forward``, ``bsa_forward_noalloc``, ``bsa_backward``, ``bsa_decode``,
-``bsa_get_status``, ``bsa_debug_timeout_probe``, ``bsa_free`` and
-``bsa_last_error``; the ``Layout`` class, ``attention``, ``attention_backward``
-and ``decode`` are conveniences over them.
+``bsa_attention_weights``, ``bsa_decode_weights``, ``bsa_evict``,
+``bsa_decode_tree``, ``bsa_get_status``, ``bsa_debug_timeout_probe``,
+``bsa_free`` and ``bsa_last_error``; the ``Layout`` class, ``attention``,
+``attention_backward``, ``decode``, ``attention_weights``, ``decode_weights``,
+``evict`` and ``decode_tree`` are conveniences over them.
 """
 from __future__ import annotations
 
@@ -36,7 +39,9 @@ STATUS_NAMES = {0: "BSA_OK", 1: "BSA_ERR_INVALID_ARG", 2: "BSA_ERR_SHAPE", 3: "B
 
 EXPORTED = ["bsa_build_layout", "bsa_layout_csr", "bsa_layout_csc", "bsa_layout_order", "bsa_layout_work",
             "bsa_layout_segments", "bsa_forward", "bsa_forward_host", "bsa_forward_noalloc", "bsa_backward",
-            "bsa_decode",
+            "bsa_decode", "bsa_attention_weights_workspace_bytes", "bsa_attention_weights",
+            "bsa_decode_weights_workspace_bytes", "bsa_decode_weights", "bsa_evict_workspace_bytes", "bsa_evict",
+            "bsa_decode_tree_workspace_bytes", "bsa_decode_tree",
             "bsa_bsbr_workspace_bytes", "bsa_bsbr_retrieval", "bsa_get_status", "bsa_debug_timeout_probe",
             "bsa_free", "bsa_last_error"]
 
@@ -93,6 +98,23 @@ def load_library(path: str = LIB_PATH):
         lib.bsa_forward_host.restype = I
         lib.bsa_decode.argtypes = [P, P, P, P, I, I, P, P, I, I, I, I, F, P, P, P]
         lib.bsa_decode.restype = I
+        S = ctypes.c_size_t
+        lib.bsa_attention_weights_workspace_bytes.argtypes = [P, I, I]
+        lib.bsa_attention_weights_workspace_bytes.restype = S
+        lib.bsa_attention_weights.argtypes = [P, P, P, P, I, I, I, I, I, F, P, S, P, S, P]
+        lib.bsa_attention_weights.restype = I
+        lib.bsa_decode_weights_workspace_bytes.argtypes = [P, I, I, I, I]
+        lib.bsa_decode_weights_workspace_bytes.restype = S
+        lib.bsa_decode_weights.argtypes = [P, P, P, P, I, I, P, P, I, I, I, I, F, P, P, P, S, P, S, P]
+        lib.bsa_decode_weights.restype = I
+        lib.bsa_evict_workspace_bytes.argtypes = [P, I, I, I]
+        lib.bsa_evict_workspace_bytes.restype = S
+        lib.bsa_evict.argtypes = [P, P, P, I, I, P, P, P, P, I, I, I, I, I, S, P, P, P, P, S, P]
+        lib.bsa_evict.restype = I
+        lib.bsa_decode_tree_workspace_bytes.argtypes = [P, I, I, I, I, I]
+        lib.bsa_decode_tree_workspace_bytes.restype = S
+        lib.bsa_decode_tree.argtypes = [P, P, P, P, P, P, I, I, P, P, P, I, I, I, I, I, F, P, P, P, S, P]
+        lib.bsa_decode_tree.restype = I
         lib.bsa_backward.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, F, P, P, P, P, P]
         lib.bsa_backward.restype = I
         lib.bsa_layout_segments.argtypes = [P, ctypes.POINTER(ctypes.POINTER(ctypes.c_int32)),
@@ -348,6 +370,239 @@ def decode(q, k_cache, v_cache, page_table, positions, layout: "Layout", batch: 
             raise BsaError(1, "page_table and positions must be contiguous int32 tensors")
     bsa_decode(q, k_cache, v_cache, page_table, page_table.shape[1], k_cache.shape[0], positions,
                layout.handle, batch, heads, kv_heads, d, scale, o, lse, stream)
+    return o, lse
+
+
+def bsa_attention_weights_workspace_bytes(layout: int, heads: int, kv_heads: int) -> int:
+    return int(load_library().bsa_attention_weights_workspace_bytes(layout, heads, kv_heads))
+
+
+def bsa_attention_weights(q, k, lse, layout: int, B: int, n: int, heads: int, kv_heads: int, d: int,
+                          scale: float, weights, weights_stride: int, workspace, workspace_bytes: int,
+                          stream=None) -> None:
+    """Enqueue the sum of the weights that a prompt's keys receive (see include/bsa.h)."""
+    lib = load_library()
+    _check(lib.bsa_attention_weights(_ptr(q), _ptr(k), _ptr(lse), layout, B, n, heads, kv_heads, d,
+                                     ctypes.c_float(scale), _ptr(weights), weights_stride, _ptr(workspace),
+                                     workspace_bytes, _stream(stream)))
+
+
+def bsa_decode_weights_workspace_bytes(layout: int, batch: int, heads: int, kv_heads: int, d: int) -> int:
+    return int(load_library().bsa_decode_weights_workspace_bytes(layout, batch, heads, kv_heads, d))
+
+
+def bsa_decode_weights(q, k_cache, v_cache, page_table, max_blocks: int, num_pages: int, positions, layout: int,
+                       batch: int, heads: int, kv_heads: int, d: int, scale: float, o, lse, weights,
+                       weights_stride: int, workspace, workspace_bytes: int, stream=None) -> None:
+    """Enqueue one decode step that adds its weights up (see include/bsa.h)."""
+    lib = load_library()
+    _check(lib.bsa_decode_weights(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), max_blocks, num_pages,
+                                  _ptr(positions), layout, batch, heads, kv_heads, d, ctypes.c_float(scale), _ptr(o),
+                                  _ptr(lse), _ptr(weights), weights_stride, _ptr(workspace), workspace_bytes,
+                                  _stream(stream)))
+
+
+def bsa_evict_workspace_bytes(layout: int, batch: int, kv_heads: int, budget: int) -> int:
+    return int(load_library().bsa_evict_workspace_bytes(layout, batch, kv_heads, budget))
+
+
+def bsa_evict(k_cache, v_cache, page_table, max_blocks: int, num_pages: int, lengths, weights, tokens, layout: int,
+              batch: int, kv_heads: int, d: int, budget: int, recent: int, stride: int, weights_out, tokens_out,
+              lengths_out, workspace, workspace_bytes: int, stream=None) -> None:
+    """Enqueue the cut of a paged cache to a budget (see include/bsa.h)."""
+    lib = load_library()
+    _check(lib.bsa_evict(_ptr(k_cache), _ptr(v_cache), _ptr(page_table), max_blocks, num_pages, _ptr(lengths),
+                         _ptr(weights), _ptr(tokens), layout, batch, kv_heads, d, budget, recent, stride,
+                         _ptr(weights_out), _ptr(tokens_out), _ptr(lengths_out), _ptr(workspace), workspace_bytes,
+                         _stream(stream)))
+
+
+def bsa_decode_tree_workspace_bytes(layout: int, batch: int, heads: int, kv_heads: int, T: int, d: int) -> int:
+    return int(load_library().bsa_decode_tree_workspace_bytes(layout, batch, heads, kv_heads, T, d))
+
+
+def bsa_decode_tree(q, k_tree, v_tree, k_cache, v_cache, page_table, max_blocks: int, num_pages: int, lengths,
+                    parents, layout: int, T: int, batch: int, heads: int, kv_heads: int, d: int, scale: float, o, lse,
+                    workspace, workspace_bytes: int, stream=None) -> None:
+    """Enqueue the attention of a tree of drafted tokens (see include/bsa.h)."""
+    lib = load_library()
+    _check(lib.bsa_decode_tree(_ptr(q), _ptr(k_tree), _ptr(v_tree), _ptr(k_cache), _ptr(v_cache), _ptr(page_table),
+                               max_blocks, num_pages, _ptr(lengths), _ptr(parents), layout, T, batch, heads, kv_heads,
+                               d, ctypes.c_float(scale), _ptr(o), _ptr(lse), _ptr(workspace), workspace_bytes,
+                               _stream(stream)))
+
+
+def _want(layout: "Layout", **tensors) -> None:
+    """Each tensor (None is skipped) on the layout's device, of its dtype and
+    shape, contiguous; ``name=(tensor, dtype, shape)``, None in a shape for any
+    size."""
+    for name, (t, dtype, shape) in tensors.items():
+        if t is None:
+            continue
+        if t.dtype != dtype or not t.is_contiguous():
+            raise BsaError(1, f"{name} must be a contiguous {str(dtype).replace('torch.', '')} tensor")
+        if t.device.type != "cuda" or t.device.index != layout.device:
+            raise BsaError(1, f"{name} is not on the layout's device (cuda:{layout.device})")
+        if len(t.shape) != len(shape) or any(w is not None and w != x for w, x in zip(shape, t.shape)):
+            want = ", ".join("any" if w is None else str(w) for w in shape)
+            raise BsaError(2, f"{name} has shape {tuple(t.shape)}, not ({want})")
+
+
+def _rows_of(layout: "Layout", rows: int, **tensors) -> int:
+    """The common distance between the rows of arrays [rows, >= n] whose last
+    dimension is contiguous (None is skipped); ``name=(tensor, dtype)``."""
+    stride = None
+    for name, (t, dtype) in tensors.items():
+        if t is None:
+            continue
+        if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or t.shape[1] < layout.n or t.stride(1) != 1:
+            raise BsaError(2, f"{name} must be a {str(dtype).replace('torch.', '')} tensor of {rows} rows of at least "
+                              f"{layout.n}, contiguous along them")
+        if t.device.type != "cuda" or t.device.index != layout.device:
+            raise BsaError(1, f"{name} is not on the layout's device (cuda:{layout.device})")
+        here = t.stride(0) if rows > 1 else layout.n
+        if stride is not None and here != stride:
+            raise BsaError(2, f"{name}: the arrays' rows must be equally far apart")
+        stride = here
+    if stride < layout.n:
+        raise BsaError(2, "rows overlap")
+    return stride
+
+
+def _on(stream):
+    """Context in which torch allocates for ``stream`` (the current one if
+    None), so that memory made here is not handed on while the work on the
+    stream still uses it."""
+    import contextlib
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _workspace(layout: "Layout", need: int, workspace):
+    """The given workspace, or a new one of ``need`` bytes; (tensor, bytes)."""
+    import torch
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=f"cuda:{layout.device}")
+    elif not workspace.is_contiguous() or workspace.device.type != "cuda" or workspace.device.index != layout.device:
+        raise BsaError(1, f"workspace must be a contiguous tensor on cuda:{layout.device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def attention_weights(q, k, lse, layout: "Layout", weights=None, scale: float | None = None, workspace=None,
+                      stream=None):
+    """torch convenience: adds to ``weights`` [kv_heads, >= n] fp32 (zeros when
+    not given) what every key of the prompt q [heads, n, d], k [kv_heads, n, d]
+    received under the forward's ``lse`` [heads, n]; returns it."""
+    import torch
+    heads, n, d = q.shape
+    kv_heads = k.shape[0]
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with _on(stream):
+        if weights is None:
+            weights = torch.zeros((kv_heads, n), dtype=torch.float32, device=q.device)
+        need = bsa_attention_weights_workspace_bytes(layout.handle, heads, kv_heads)
+        workspace, size = _workspace(layout, need, workspace)
+    _want(layout, q=(q, torch.bfloat16, (heads, layout.n, d)), k=(k, torch.bfloat16, (kv_heads, layout.n, d)),
+          lse=(lse, torch.float32, (heads, layout.n)))
+    stride = _rows_of(layout, kv_heads, weights=(weights, torch.float32))
+    bsa_attention_weights(q, k, lse, layout.handle, layout.B, n, heads, kv_heads, d, scale, weights, stride,
+                          workspace, size, stream)
+    return weights
+
+
+def decode_weights(q, k_cache, v_cache, page_table, positions, layout: "Layout", batch: int, weights,
+                   scale: float | None = None, o=None, lse=None, workspace=None, stream=None):
+    """torch convenience: ``decode`` that also adds the step's weights to
+    ``weights`` [batch * H_kv, >= n] fp32; returns (o, lse)."""
+    import torch
+    heads, d = q.shape
+    hkv = k_cache.shape[1]
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    pages = k_cache.shape[0]
+    with _on(stream):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((heads,), dtype=torch.float32, device=q.device)
+        need = bsa_decode_weights_workspace_bytes(layout.handle, batch, heads, batch * hkv, d)
+        workspace, size = _workspace(layout, need, workspace)
+    _want(layout, q=(q, torch.bfloat16, (heads, d)), k_cache=(k_cache, torch.bfloat16, (pages, hkv, layout.B, d)),
+          v_cache=(v_cache, torch.bfloat16, (pages, hkv, layout.B, d)), o=(o, torch.bfloat16, (heads, d)),
+          lse=(lse, torch.float32, (heads,)), page_table=(page_table, torch.int32, (batch, None)),
+          positions=(positions, torch.int32, (batch,)))
+    stride = _rows_of(layout, batch * hkv, weights=(weights, torch.float32))
+    bsa_decode_weights(q, k_cache, v_cache, page_table, page_table.shape[1], pages, positions, layout.handle, batch,
+                       heads, batch * hkv, d, scale, o, lse, weights, stride, workspace, size, stream)
+    return o, lse
+
+
+def evict(k_cache, v_cache, page_table, lengths, weights, layout: "Layout", budget: int, recent: int = 0,
+          tokens=None, weights_out=None, tokens_out=None, lengths_out=None, workspace=None, stream=None):
+    """torch convenience: cuts the caches [pages, H_kv, B, d] in place to
+    ``budget`` tokens per key/value head by ``weights`` [batch * H_kv, >= n];
+    returns (weights_out, tokens_out, lengths_out), allocating what is not
+    given.  The outputs are not the inputs: they are the next call's inputs."""
+    import torch
+    batch = lengths.shape[0]
+    pages, hkv, _, d = k_cache.shape
+    rows = batch * hkv
+
+    def like(dtype):
+        # an output that is not given has its rows as far apart as the weights'
+        return torch.empty_strided(weights.shape, weights.stride(), dtype=dtype, device=weights.device)
+
+    with _on(stream):
+        if weights_out is None:
+            weights_out = like(torch.float32)
+        if tokens_out is None:
+            tokens_out = like(torch.int32)
+        if lengths_out is None:
+            lengths_out = torch.empty_like(lengths)
+        need = bsa_evict_workspace_bytes(layout.handle, batch, rows, budget)
+        workspace, size = _workspace(layout, need, workspace)
+    _want(layout, k_cache=(k_cache, torch.bfloat16, (pages, hkv, layout.B, d)),
+          v_cache=(v_cache, torch.bfloat16, (pages, hkv, layout.B, d)),
+          page_table=(page_table, torch.int32, (batch, None)), lengths=(lengths, torch.int32, (batch,)),
+          lengths_out=(lengths_out, torch.int32, (batch,)))
+    stride = _rows_of(layout, rows, weights=(weights, torch.float32), tokens=(tokens, torch.int32),
+                      weights_out=(weights_out, torch.float32), tokens_out=(tokens_out, torch.int32))
+    bsa_evict(k_cache, v_cache, page_table, page_table.shape[1], pages, lengths, weights, tokens, layout.handle,
+              batch, rows, d, budget, recent, stride, weights_out, tokens_out, lengths_out, workspace, size, stream)
+    return weights_out, tokens_out, lengths_out
+
+
+def decode_tree(q, k_tree, v_tree, k_cache, v_cache, page_table, lengths, parents, layout: "Layout",
+                scale: float | None = None, o=None, lse=None, workspace=None, stream=None):
+    """torch convenience: q [batch * H, T, d], k_tree, v_tree [batch * H_kv, T,
+    d], caches [pages, H_kv, B, d] bf16; lengths [batch], parents [batch, T]
+    int32; returns (o, lse).  Rows whose parent is -2 are not written."""
+    import torch
+    heads, T, d = q.shape
+    batch = lengths.shape[0]
+    pages, hkv = k_cache.shape[:2]
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with _on(stream):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((heads, T), dtype=torch.float32, device=q.device)
+        need = bsa_decode_tree_workspace_bytes(layout.handle, batch, heads, batch * hkv, T, d)
+        workspace, size = _workspace(layout, need, workspace)
+    tree = (batch * hkv, T, d)
+    _want(layout, q=(q, torch.bfloat16, (heads, T, d)), k_tree=(k_tree, torch.bfloat16, tree),
+          v_tree=(v_tree, torch.bfloat16, tree), k_cache=(k_cache, torch.bfloat16, (pages, hkv, layout.B, d)),
+          v_cache=(v_cache, torch.bfloat16, (pages, hkv, layout.B, d)), o=(o, torch.bfloat16, (heads, T, d)),
+          lse=(lse, torch.float32, (heads, T)), page_table=(page_table, torch.int32, (batch, None)),
+          lengths=(lengths, torch.int32, (batch,)), parents=(parents, torch.int32, (batch, T)))
+    bsa_decode_tree(q, k_tree, v_tree, k_cache, v_cache, page_table, page_table.shape[1], pages, lengths, parents,
+                    layout.handle, T, batch, heads, batch * hkv, d, scale, o, lse, workspace, size, stream)
     return o, lse
 
 

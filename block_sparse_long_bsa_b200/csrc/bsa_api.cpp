@@ -195,6 +195,12 @@ static int check_device(const bsa_layout* layout) {
   return BSA_OK;
 }
 
+}  // extern "C"
+
+int bsa::check_layout_device(const bsa_layout* layout) { return check_device(layout); }
+
+extern "C" {
+
 int bsa_layout_segments(const bsa_layout* layout, const int32_t** seg_ptr, const int32_t** segs,
                         int* layout_heads, int* count) {
   if (!layout) return set_error(BSA_ERR_INVALID_ARG, "layout is NULL");

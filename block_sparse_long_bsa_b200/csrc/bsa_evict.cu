@@ -1,0 +1,427 @@
+// Cutting a paged key/value cache to a budget by accumulated attention weight
+// (sm_100a): every key/value head of every sequence keeps its `budget` cached
+// tokens, the `recent` newest and then those of largest weight, moved into
+// its first slots.
+//
+// A kept token that lies below the budget stays where it is; the kept ones
+// behind it move into the holes, the i-th hole taking the i-th of them.  So a
+// row is read only behind the budget and written only below it: every move is
+// independent of the others, and as few as possible are made (attention does
+// not ask for the order of its keys; `tokens` says which token a slot holds).
+//
+// Kernel 1 (select_kernel), a block per (sequence, key/value head): weights
+// become 32-bit keys whose unsigned order is theirs (protected tokens above
+// all), held in shared memory; the budget-th largest is found digit by digit
+// (11, 11 and 10 bits, a histogram each); ties at it go to the lowest slots;
+// ranks of holes and movers come from ballots and a scan over the warps.
+// Kernel 2 (move_kernel), a warp per 32 slots: new weights, tokens and
+// lengths, and the moved rows, 16 bytes a lane.  Its bound is memory: 4 d
+// bytes read and written a moved token.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <mutex>
+#include <string>
+
+#include "bsa_internal.h"
+
+namespace bsa {
+namespace evict {
+
+constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kKeysInSmem = 48 * 1024;          // longer rows recompute their keys in every pass
+constexpr int kMoveThreads = 256;
+
+struct Params {
+  __nv_bfloat16* kc;
+  __nv_bfloat16* vc;
+  const int32_t* page_table;
+  const int32_t* lengths;
+  const float* weights;
+  const int32_t* tokens;      // null: slot s holds token s
+  float* weights_out;
+  int32_t* tokens_out;
+  int32_t* lengths_out;
+  int32_t* src;               // [rows][cap]: the slot that slot s takes its token from
+  int32_t* movers;            // [rows][cap]
+  int4* meta;                 // [rows]: kept, newest token, 1 if refused, 1 if nothing moves
+  uint32_t* status;
+  size_t stride;              // of weights, tokens and their outputs
+  int n, B, max_blocks, num_pages, hkv, budget, recent, cap;
+};
+
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Order-preserving key of a weight; a NaN counts as -inf, -0 as 0.
+__device__ __forceinline__ uint32_t key_of(float w) {
+  if (w != w) w = -INFINITY;
+  const uint32_t b = w == 0.f ? 0u : __float_as_uint(w);
+  return b >> 31 ? ~b : b | 0x80000000u;
+}
+
+__global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const Params p) {
+  extern __shared__ uint32_t s_keys[];
+  __shared__ int hist[kBins];
+  __shared__ int s_red[kSelWarps], s_red2[kSelWarps];
+  __shared__ int s_bad, s_newest, s_digit, s_left;
+  grid_release();
+  const int row = blockIdx.x;
+  const int b = row / p.hkv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int len = p.lengths[b];
+  const float* w = p.weights + size_t(row) * p.stride;
+  const int32_t* tok = p.tokens ? p.tokens + size_t(row) * p.stride : nullptr;
+  if (tid == 0) {
+    s_bad = len < 0 || len > p.n;
+    s_newest = INT32_MIN;
+  }
+  __syncthreads();
+  if (!s_bad && len > p.budget) {
+    bool bad = false;
+    for (int j = tid; j < (len + p.B - 1) / p.B; j += kSelThreads) {
+      const int pg = p.page_table[size_t(b) * p.max_blocks + j];
+      bad |= pg < 0 || pg >= p.num_pages;
+    }
+    if (bad) s_bad = 1;
+  }
+  __syncthreads();
+  if (s_bad) {
+    if (tid == 0) {
+      p.meta[row] = make_int4(0, 0, 1, 1);
+      atomicOr(p.status, kStatusBadIndex);
+    }
+    return;
+  }
+  // the newest token, from which the protected ones are counted back
+  int newest = len - 1;
+  if (tok) {
+    int m = INT32_MIN;
+    for (int s = tid; s < len; s += kSelThreads) m = max(m, tok[s]);
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lane == 0) atomicMax(&s_newest, m);
+    __syncthreads();
+    newest = len > 0 ? s_newest : -1;
+  }
+  if (len <= p.budget) {
+    if (tid == 0) p.meta[row] = make_int4(len, newest, 0, 1);
+    return;
+  }
+  const int64_t floor_tok = int64_t(newest) - p.recent;      // tokens above it are protected
+  auto make_key = [&](int s) -> uint32_t {
+    const int t = tok ? tok[s] : s;
+    return int64_t(t) > floor_tok ? 0xffffffffu : key_of(w[s]);
+  };
+  const bool held = len <= kKeysInSmem;
+  if (held)
+    for (int s = tid; s < len; s += kSelThreads) s_keys[s] = make_key(s);
+  auto key_at = [&](int s) -> uint32_t { return held ? s_keys[s] : make_key(s); };
+
+  // ---- the budget-th largest key, from the highest digit down
+  uint32_t prefix = 0, mask = 0;
+  int left = p.budget;                   // how many of the keys under the prefix are kept
+  const int shifts[3] = {21, 10, 0}, bits[3] = {11, 11, 10};
+#pragma unroll
+  for (int d = 0; d < 3; ++d) {
+    for (int x = tid; x < kBins; x += kSelThreads) hist[x] = 0;
+    __syncthreads();
+    const uint32_t dm = (1u << bits[d]) - 1u;
+    for (int s0 = 0; s0 < len; s0 += kSelThreads) {
+      const int s = s0 + tid;
+      const uint32_t k = s < len ? key_at(s) : 0u;
+      const bool in = s < len && (k & mask) == prefix;
+      const int bin = in ? int(k >> shifts[d] & dm) : -1;
+      // one bin for the whole warp (a run of equal weights) is one addition
+      int same;
+      __match_all_sync(0xffffffffu, bin, &same);
+      if (same) {
+        if (lane == 0 && bin >= 0) atomicAdd(&hist[bin], 32);
+      } else if (in) {
+        atomicAdd(&hist[bin], 1);
+      }
+    }
+    __syncthreads();
+    // the digit whose keys from above reach `left`: each thread owns two bins,
+    // thread 0 the highest ones
+    const int hi_bin = kBins - 1 - 2 * tid;
+    const int a = hist[hi_bin], c = hist[hi_bin - 1];
+    int sum = a + c;
+#pragma unroll
+    for (int off = 1; off < 32; off *= 2) {
+      const int y = __shfl_up_sync(0xffffffffu, sum, off);
+      if (lane >= off) sum += y;
+    }
+    if (lane == 31) s_red[warp] = sum;
+    __syncthreads();
+    int before = 0;
+    for (int x = 0; x < warp; ++x) before += s_red[x];
+    const int incl = before + sum, excl = incl - a - c;      // keys in higher bins than the thread's
+    if (excl < left && left <= incl) {
+      const bool first = left <= excl + a;
+      s_digit = first ? hi_bin : hi_bin - 1;
+      s_left = first ? left - excl : left - excl - a;
+    }
+    __syncthreads();
+    prefix |= uint32_t(s_digit) << shifts[d];
+    mask |= dm << shifts[d];
+    left = s_left;
+    __syncthreads();
+  }
+  // keys above `prefix` are kept, and of those equal to it the first `left`
+
+  // ---- ranks: each warp owns a run of slots
+  const int per = (len + kSelWarps * 32 - 1) / (kSelWarps * 32) * 32;
+  const int lo = min(len, warp * per), hi = min(len, lo + per);
+  auto scan_warps = [&](int* red, int count, int& total) -> int {   // exclusive prefix over the warps
+    if (lane == 0) red[warp] = count;
+    __syncthreads();
+    int pre = 0;
+    total = 0;
+    for (int x = 0; x < kSelWarps; ++x) {
+      if (x < warp) pre += red[x];
+      total += red[x];
+    }
+    return pre;
+  };
+  int count = 0, total = 0;
+  for (int s0 = lo; s0 < hi; s0 += 32) {
+    const int s = s0 + lane;
+    count += __popc(__ballot_sync(0xffffffffu, s < hi && key_at(s) == prefix));
+  }
+  const int ties = scan_warps(s_red, count, total);
+  // kept slots of a ballot, with the ties seen so far
+  auto kept_of = [&](int s0, int& seen) -> unsigned {
+    const int s = s0 + lane;
+    const uint32_t k = s < hi ? key_at(s) : 0u;
+    const unsigned eq = __ballot_sync(0xffffffffu, s < hi && k == prefix);
+    const bool take = s < hi && (k > prefix || (k == prefix && seen + __popc(eq & ((1u << lane) - 1u)) < left));
+    seen += __popc(eq);
+    return __ballot_sync(0xffffffffu, take);
+  };
+  int holes = 0, movers = 0, seen = ties;
+  for (int s0 = lo; s0 < hi; s0 += 32) {
+    const unsigned kept = kept_of(s0, seen);
+    // slots of this ballot that lie below the budget
+    const int below = min(32, max(0, min(p.budget, hi) - s0));
+    const unsigned low = below == 32 ? 0xffffffffu : (1u << below) - 1u;
+    holes += __popc(~kept & low);
+    movers += __popc(kept & ~low);
+  }
+  int hole0 = scan_warps(s_red2, holes, total);
+  __syncthreads();
+  int mover0 = scan_warps(s_red, movers, total);
+  int32_t* const mv = p.movers + size_t(row) * p.cap;
+  int32_t* const src = p.src + size_t(row) * p.cap;
+  seen = ties;
+  for (int s0 = lo; s0 < hi; s0 += 32) {
+    const unsigned kept = kept_of(s0, seen);
+    const int s = s0 + lane;
+    const bool is = kept >> lane & 1u;
+    const unsigned moves = __ballot_sync(0xffffffffu, is && s >= p.budget);
+    if (is && s >= p.budget) mv[mover0 + __popc(moves & ((1u << lane) - 1u))] = s;
+    mover0 += __popc(moves);
+  }
+  __syncthreads();                       // the movers are in memory for the whole block
+  seen = ties;
+  for (int s0 = lo; s0 < min(hi, p.budget); s0 += 32) {
+    const unsigned kept = kept_of(s0, seen);
+    const int s = s0 + lane;
+    const bool hole = s < hi && s < p.budget && !(kept >> lane & 1u);
+    const unsigned hb = __ballot_sync(0xffffffffu, hole);
+    if (s < hi && s < p.budget) src[s] = hole ? mv[hole0 + __popc(hb & ((1u << lane) - 1u))] : s;
+    hole0 += __popc(hb);
+  }
+  if (tid == 0) p.meta[row] = make_int4(p.budget, newest, 0, 0);
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const Params p, int tiles) {
+  constexpr int LPR = HD / 8;            // lanes of a row, 16 bytes each
+  constexpr int SPI = 32 / (2 * LPR);    // tokens a warp moves at once (key and value)
+  const int row = blockIdx.x / tiles, tile = blockIdx.x - row * tiles;
+  const int b = row / p.hkv, hk = row - b * p.hkv;
+  const int lane = threadIdx.x & 31;
+  const int s = tile * kMoveThreads + threadIdx.x;
+  grid_wait();
+  const int4 m = p.meta[row];
+  if (m.z) {                             // refused: left as it was
+    if (tile == 0 && threadIdx.x == 0 && hk == 0) p.lengths_out[b] = -1;
+    return;
+  }
+  if (tile == 0 && threadIdx.x == 0 && hk == 0) p.lengths_out[b] = m.x;
+  const size_t at = size_t(row) * p.stride;
+  int from = s;
+  if (s < p.n) {
+    float wt = 0.f;
+    int t = int(int64_t(m.y) + 1 + (s - m.x));               // a slot behind takes the next token to come
+    if (s < m.x) {
+      if (!m.w) from = p.src[size_t(row) * p.cap + s];
+      wt = p.weights[at + from];
+      t = p.tokens ? p.tokens[at + from] : from;
+    }
+    p.weights_out[at + s] = wt;
+    p.tokens_out[at + s] = t;
+  }
+  unsigned todo = __ballot_sync(0xffffffffu, from != s);
+  if (!todo) return;
+  // rows of the caches, counted in d-element rows (64-bit: long caches pass 2^31 elements)
+  int64_t to_row = 0, from_row = 0;
+  if (from != s) {
+    const int32_t* pt = p.page_table + size_t(b) * p.max_blocks;
+    to_row = (int64_t(pt[s / p.B]) * p.hkv + hk) * p.B + s % p.B;
+    from_row = (int64_t(pt[from / p.B]) * p.hkv + hk) * p.B + from % p.B;
+  }
+  const int sub = lane / (2 * LPR), in = lane % (2 * LPR);
+  uint4* const base = reinterpret_cast<uint4*>(in < LPR ? p.kc : p.vc) + in % LPR;
+  while (todo) {
+    constexpr int U = 4;                 // tokens in flight, times SPI
+    uint4 v[U];
+    int64_t dst[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // SPI tokens of the ballot: one for each part of the warp
+      int x = -1;
+#pragma unroll
+      for (int y = 0; y < SPI; ++y) {
+        const int first = todo ? __ffs(todo) - 1 : -1;
+        if (todo) todo &= todo - 1;
+        if (y == sub) x = first;
+      }
+      const int64_t f = __shfl_sync(0xffffffffu, from_row, x & 31);
+      dst[u] = __shfl_sync(0xffffffffu, to_row, x & 31);
+      if (x < 0) dst[u] = -1;
+      else v[u] = base[f * LPR];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (dst[u] >= 0) base[dst[u] * LPR] = v[u];
+  }
+}
+
+bool aligned(const void* x, uintptr_t a) { return (reinterpret_cast<uintptr_t>(x) % a) == 0; }
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+int check_sizes(const bsa_layout* layout, int batch, int kv_heads, int budget) {
+  if (!layout) return set_error(BSA_ERR_INVALID_ARG, "layout is NULL");
+  if (layout->B != 64 && layout->B != 128) return set_error(BSA_ERR_UNSUPPORTED, "B must be 64 or 128");
+  if (batch < 1 || kv_heads < 1) return set_error(BSA_ERR_SHAPE, "batch and kv_heads must be >= 1");
+  if (kv_heads % batch) return set_error(BSA_ERR_SHAPE, "kv_heads must be a multiple of batch");
+  if (budget < 1) return set_error(BSA_ERR_SHAPE, "budget must be >= 1");
+  if (int64_t(kv_heads) * ((int64_t(layout->n) + kMoveThreads - 1) / kMoveThreads) > INT32_MAX)
+    return set_error(BSA_ERR_SHAPE, "too many slots");
+  return BSA_OK;
+}
+
+size_t bytes_of(const bsa_layout* layout, int kv_heads, int budget, size_t* movers, size_t* meta) {
+  const size_t list = up256(size_t(kv_heads) * std::min(budget, layout->n) * 4);
+  *movers = list;
+  *meta = 2 * list;
+  return 2 * list + size_t(kv_heads) * sizeof(int4);
+}
+
+int launch(const Params& p, int rows, int d, cudaStream_t stream) {
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= 64) return set_error(BSA_ERR_CUDA, "cannot query the device");
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev]) {
+      e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysInSmem * 4);
+      if (e != cudaSuccess) return set_error(BSA_ERR_CUDA, std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e));
+      done[dev] = true;
+    }
+  }
+  const size_t smem = size_t(p.n <= kKeysInSmem ? p.n : kKeysInSmem) * 4;
+  select_kernel<<<unsigned(rows), kSelThreads, smem, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return set_error(BSA_ERR_CUDA, std::string("eviction select launch: ") + cudaGetErrorString(e));
+  const int tiles = (p.n + kMoveThreads - 1) / kMoveThreads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(rows) * unsigned(tiles), 1, 1);
+  cfg.blockDim = dim3(kMoveThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = d == 128 ? cudaLaunchKernelEx(&cfg, move_kernel<128>, p, tiles) : cudaLaunchKernelEx(&cfg, move_kernel<64>, p, tiles);
+  if (e != cudaSuccess) return set_error(BSA_ERR_CUDA, std::string("eviction move launch: ") + cudaGetErrorString(e));
+  return BSA_OK;
+}
+
+}  // namespace evict
+}  // namespace bsa
+
+extern "C" {
+
+size_t bsa_evict_workspace_bytes(const bsa_layout* layout, int batch, int kv_heads, int budget) {
+  if (bsa::evict::check_sizes(layout, batch, kv_heads, budget) != BSA_OK) return 0;
+  size_t a, b;
+  return bsa::evict::bytes_of(layout, kv_heads, budget, &a, &b);
+}
+
+int bsa_evict(void* k_cache, void* v_cache, const int32_t* page_table, int max_blocks, int num_pages,
+              const int32_t* lengths, const float* weights, const int32_t* tokens, const bsa_layout* layout, int batch,
+              int kv_heads, int d, int budget, int recent, size_t stride, float* weights_out, int32_t* tokens_out,
+              int32_t* lengths_out, void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace bsa;
+  if (!layout) return set_error(BSA_ERR_INVALID_ARG, "layout is NULL");
+  int st = evict::check_sizes(layout, batch, kv_heads, budget);
+  if (st != BSA_OK) return st;
+  if (d != 64 && d != 128) return set_error(BSA_ERR_UNSUPPORTED, "d must be 64 or 128");
+  if (recent < 0 || recent > budget) return set_error(BSA_ERR_SHAPE, "recent must lie in [0, budget]");
+  if (max_blocks < layout->nb) return set_error(BSA_ERR_SHAPE, "max_blocks is smaller than the layout's blocks");
+  if (num_pages < 1) return set_error(BSA_ERR_SHAPE, "num_pages must be >= 1");
+  if (stride < size_t(layout->n)) return set_error(BSA_ERR_SHAPE, "stride is smaller than the layout's n");
+  if (!k_cache || !v_cache || !page_table || !lengths || !weights || !weights_out || !tokens_out || !lengths_out ||
+      !workspace)
+    return set_error(BSA_ERR_INVALID_ARG, "null pointer");
+  if (!evict::aligned(k_cache, 16) || !evict::aligned(v_cache, 16) || !evict::aligned(workspace, 16))
+    return set_error(BSA_ERR_INVALID_ARG, "k_cache, v_cache and workspace must be 16-byte aligned");
+  for (const void* x : {static_cast<const void*>(page_table), static_cast<const void*>(lengths),
+                        static_cast<const void*>(weights), static_cast<const void*>(tokens),
+                        static_cast<const void*>(weights_out), static_cast<const void*>(tokens_out),
+                        static_cast<const void*>(lengths_out)})
+    if (!evict::aligned(x, 4)) return set_error(BSA_ERR_INVALID_ARG, "arrays must be 4-byte aligned");
+  if (weights_out == weights || tokens_out == tokens || lengths_out == lengths)
+    return set_error(BSA_ERR_INVALID_ARG, "weights_out, tokens_out and lengths_out must not be the inputs");
+  size_t movers = 0, meta = 0;
+  const size_t need = evict::bytes_of(layout, kv_heads, budget, &movers, &meta);
+  if (workspace_bytes < need)
+    return set_error(BSA_ERR_SHAPE, "workspace too small: " + std::to_string(need) + " bytes needed");
+  st = check_layout_device(layout);
+  if (st != BSA_OK) return st;
+  evict::Params p{};
+  p.kc = static_cast<__nv_bfloat16*>(k_cache);
+  p.vc = static_cast<__nv_bfloat16*>(v_cache);
+  p.page_table = page_table;
+  p.lengths = lengths;
+  p.weights = weights;
+  p.tokens = tokens;
+  p.weights_out = weights_out;
+  p.tokens_out = tokens_out;
+  p.lengths_out = lengths_out;
+  char* w = static_cast<char*>(workspace);
+  p.src = reinterpret_cast<int32_t*>(w);
+  p.movers = reinterpret_cast<int32_t*>(w + movers);
+  p.meta = reinterpret_cast<int4*>(w + meta);
+  p.status = layout->d_status;
+  p.stride = stride;
+  p.n = layout->n;
+  p.B = layout->B;
+  p.max_blocks = max_blocks;
+  p.num_pages = num_pages;
+  p.hkv = kv_heads / batch;
+  p.budget = budget;
+  p.recent = recent;
+  p.cap = std::min(budget, layout->n);
+  return evict::launch(p, kv_heads, d, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

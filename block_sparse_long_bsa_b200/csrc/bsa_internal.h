@@ -66,6 +66,9 @@ namespace bsa {
 // Thread-local error message; returns the status for convenience.
 int set_error(int status, const std::string& msg);
 
+// BSA_OK if the layout is on the current device, else an error (bsa_api.cpp).
+int check_layout_device(const bsa_layout* layout);
+
 // Host layout compiler (bsa_layout.cpp).  Fills row_ptr/col_idx/order/work/max_row.
 int compile_layout(const bsa_pattern& spec, int n, int B, int L, bsa_layout* out);
 

@@ -1,0 +1,1099 @@
+// Attention over the paged key/value cache with the reads of one call split
+// over the GPU (sm_100a): the decode step that also adds up the weights it
+// gives to the cached keys (bsa_decode_weights), and the attention of a tree
+// of drafted tokens over the cache and their own ancestors (bsa_decode_tree).
+//
+// Both have a few query rows per key/value head (the group's query heads times
+// the tree's tokens) against all the cached keys that the rows' layout row
+// keeps, so what bounds them is the read of the kept pages, 4 d bytes a key.
+// A unit is (sequence, key/value head or query head, 128-row tile, layout
+// row): the rows of a tile that share a layout row read the same keys, and no
+// key of another route ever meets them, so nothing but the end of the cache
+// has to be masked.  The unit's list of 64-key chunks is cut into S runs, one
+// CTA each.
+//
+// Kernel 1 (paged_attention_kernel), per 64-key chunk of a run:
+//   S = Q K^T                  (tcgen05.mma, bf16 x bf16 -> fp32 in TMEM)
+//   m' = max(m, rowmax S), P = exp2((S - m') scale log2 e)
+//   O += P V                   (tcgen05.mma, A = P from TMEM)
+// with P written as two bf16 numbers (its upper 16 bits and the rounding of what
+// they leave, within 2^-15 of P together) over the 64 columns of S, and two
+// products: the step is bound by the cache's bytes, so the second product
+// costs nothing that shows, and o is then rounded once, at its end.  A run
+// leaves its unnormalised O, m and l in the caller's workspace; the step
+// leaves the scores too.
+// Kernel 2 joins the runs of each row.  The tree's rows add their ancestors
+// there, at most T keys each, on the plain cores in fp32: an ancestor's key
+// and value are read by the rows that descend from it and by no others, so a
+// branch's infinity cannot reach another branch.  The step's kernel 2 also
+// turns the scores into weights, p = exp2(s scale log2 e - M) / L.
+//
+// Roles of kernel 1 (192 threads, two CTAs per SM): warp 0 looks the pages up
+// and issues the TMA loads, warp 1 issues the products, warps 2-5 hold one
+// query row per thread.  Every wait is bounded, as in the forward.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+#include <string>
+
+#include "bsa_device.cuh"
+#include "bsa_internal.h"
+#include "bsa_tmap.h"
+
+namespace bsa {
+namespace paged {
+
+using namespace ptx;
+
+constexpr int kThreads = 192;
+constexpr int kTileM = 128;            // query rows of a tile (tcgen05 M = 128)
+constexpr int kChunk = 64;             // keys per chunk
+constexpr int kKS = 2, kVS = 3;        // K and V slots in shared memory
+constexpr int kMaxT = 128;             // drafted tokens at most
+constexpr float kRescaleThreshold = 8.0f;
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr uint64_t kWaitNs = 1000000000ull, kDrainNs = 200000000ull;
+
+// Runs of a unit: as many CTAs as the GPU holds at once (two on each of 148
+// SMs) shared out over the units, and no run longer than kRunChunks, so that
+// sequences of other lengths and the end of the grid level out.
+constexpr int kSlots = 2 * 148;
+constexpr int kRunChunks = 32;
+
+struct Plan {
+  int hg;          // head groups of a sequence: key/value heads, or query heads when routes differ by head
+  int hpt;         // query heads that share a tile
+  int rows;        // query rows of a head group
+  int mtiles;      // 128-row tiles of them
+  int groups;      // layout rows that a tree's positions can fall in
+  int units;       // batch * hg * mtiles * groups
+  int S;           // runs of a unit
+  int cap;         // rows of a partial result
+};
+
+Plan plan_of(const bsa_layout* L, int batch, int heads, int kv_heads, int T) {
+  Plan p{};
+  const int H = heads / batch, hkv = kv_heads / batch;
+  p.hpt = L->L == 1 ? H / hkv : 1;
+  p.hg = H / p.hpt;
+  p.rows = p.hpt * T;
+  p.mtiles = (p.rows + kTileM - 1) / kTileM;
+  p.groups = (T + L->B - 2) / L->B + 1;
+  const int64_t busy = int64_t(batch) * p.hg * p.mtiles;
+  p.units = int(std::min<int64_t>(busy * p.groups, INT32_MAX));
+  const int chunks = std::max(1, L->max_row * (L->B / kChunk));
+  const int fill = int(std::min<int64_t>(chunks, std::max<int64_t>(1, (kSlots + busy - 1) / busy)));
+  p.S = std::max(fill, (chunks + kRunChunks - 1) / kRunChunks);
+  p.cap = std::min(kTileM, p.rows);
+  return p;
+}
+
+struct Offsets {
+  size_t ml, flag, scores, total;      // bytes; O starts at 0
+};
+inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+Offsets offsets_of(const Plan& p, const bsa_layout* L, int heads, int d, bool scores) {
+  Offsets o{};
+  const size_t runs = size_t(p.units) * p.S, rows = runs * p.cap;
+  o.ml = up256(rows * d * 4);
+  o.flag = o.ml + up256(rows * 8);
+  o.scores = o.flag + up256(runs * 4);
+  o.total = o.scores + (scores ? up256(size_t(heads) * L->max_row * L->B * 4) : 0);
+  return o;
+}
+
+struct Params {
+  const int32_t* page_table;
+  const int32_t* lengths;      // step: the new token's position; tree: cached tokens
+  const int32_t* parents;      // tree: [batch][T]
+  const int32_t* row_ptr;
+  const int32_t* col_idx;
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k_tree;
+  const __nv_bfloat16* v_tree;
+  __nv_bfloat16* o;
+  float* lse;
+  float* weights;
+  size_t weights_stride;
+  float* part_o;               // [unit][run][cap][d]
+  float2* part_ml;             // [unit][run][cap]
+  int* part_flag;              // [unit][run]
+  float* scores;               // step: [heads][max_row * B]
+  uint32_t* status;
+  size_t score_stride;
+  int n, nb, L, H, hkv, max_blocks, num_pages, max_row;
+  int hg, hpt, rows, mtiles, groups, S, cap, T, tiles;
+  float scale_log2;
+};
+
+template <int BLK, int HD>
+struct Shape {
+  static constexpr int kCPB = BLK / kChunk;
+  static constexpr int kQBytes = kTileM * HD * 2;
+  static constexpr int kTileBytes = kChunk * HD * 2;
+  static constexpr int kAtomQ = kTileM * 128, kAtomKV = kChunk * 128;
+  static constexpr int kOffK = kQBytes;
+  static constexpr int kOffV = kOffK + kKS * kTileBytes;
+  static constexpr int kOffBar = kOffV + kVS * kTileBytes;
+  // q_full, k_full[KS], v_full[VS], s_full[2], p_full[2], o_done[VS], drain
+  static constexpr int kNumBars = 1 + kKS + kVS + 2 + 2 + kVS + 1;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // TMEM address, abort flag, page flag, deepest token
+  static constexpr int kOffRun = kOffMisc + 16;
+  static constexpr int kOffJump = kOffRun + 32;              // the tree's walk, a byte a token
+  static constexpr int kOffDepth = kOffJump + kMaxT;
+  static constexpr int kSmem = kOffDepth + kMaxT;
+  static constexpr int kColS = 0, kColO = 2 * kChunk;
+  static constexpr uint32_t kTmemCols = 256;
+  static constexpr uint32_t kIdescQK = idesc_bf16(kTileM, kChunk, 0, 0);
+  static constexpr uint32_t kIdescPV = idesc_bf16(kTileM, HD, 0, 1);
+  static_assert(2 * kChunk + HD <= 256, "TMEM budget");
+  static_assert(kKS == 2, "s_full doubles as the release of a K slot");
+};
+
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ void bf16x2_to_f32(uint32_t w, float& lo, float& hi) {
+  lo = __uint_as_float(w << 16);
+  hi = __uint_as_float(w & 0xffff0000u);
+}
+
+// What cutting a probability's low 16 bits off leaves, and never 0: an
+// infinite value that the row reads then has the same sign in both products
+// (a rounded first part could leave a negative rest, and 0 * inf is NaN).
+// P itself being 0, where exp2 underflows, is 0 * inf in the definition too.
+__device__ __forceinline__ float rest_of(uint32_t bits) {
+  return fmaxf(__uint_as_float(bits) - __uint_as_float(bits & 0xffff0000u), 1e-30f);
+}
+
+// What a CTA of kernel 1 works on, found by one thread and shared.
+struct Run {
+  int start;       // first list entry of the unit's layout row
+  int c0, c1;      // the run's chunks, counted in the unit's list
+  int tail;        // valid keys of the list's last chunk
+  int last;        // index of the list's last chunk
+  int go;          // 0: nothing to do and nothing will be read
+};
+
+// Depth of every drafted token by pointer jumping: after round k a token
+// points 2^k ancestors up.  A parent that is not an earlier token ends the
+// walk (kernel 2 refuses such a token).  Called by all threads.
+__device__ __forceinline__ int deepest(const int32_t* parents, int T, volatile int8_t* jump, volatile int8_t* depth,
+                                       int* most) {
+  const int i = threadIdx.x;
+  static_assert(kMaxT <= 128, "a token's index and depth fit a signed byte");
+  if (i < kMaxT) {
+    const int par = i < T ? parents[i] : -1;
+    const bool up = par >= 0 && par < i;
+    jump[i] = int8_t(up ? par : -1);
+    depth[i] = int8_t(up ? 1 : 0);
+  }
+  if (i == 0) *most = 0;
+  __syncthreads();
+  for (int step = 1; step < T; step *= 2) {
+    int to = -1, add = 0;
+    if (i < kMaxT && jump[i] >= 0) {
+      to = jump[jump[i]];
+      add = depth[jump[i]];
+    }
+    __syncthreads();
+    if (i < kMaxT && jump[i] >= 0) {
+      jump[i] = int8_t(to);
+      depth[i] = int8_t(depth[i] + add);
+    }
+    __syncthreads();
+  }
+  if (i < T) atomicMax(most, int(depth[i]));
+  __syncthreads();
+  return *most;
+}
+
+template <int BLK, int HD, bool TREE>
+__global__ void __launch_bounds__(kThreads, 2)
+    paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                           const __grid_constant__ CUtensorMap tmV, const Params p) {
+  using S = Shape<BLK, HD>;
+  constexpr int CPB = S::kCPB;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_addr(smem);
+  if (base & 1023u) {                    // never expected: the swizzle needs 1024-byte aligned tiles
+    if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
+    return;
+  }
+  grid_release();
+  const int run = blockIdx.x % p.S;
+  const int unit = blockIdx.x / p.S;
+  const int grp = unit % p.groups;
+  const int mt = unit / p.groups % p.mtiles;
+  const int bh = unit / p.groups / p.mtiles;      // (sequence, head group)
+  const int b = bh / p.hg, hg = bh - b * p.hg;
+  const int f0 = b * p.H + hg * p.hpt;            // first query head of the tile
+  const int hk = p.L == 1 ? hg : hg / (p.H / p.hkv);
+  const int vr = min(kTileM, p.rows - mt * kTileM);   // rows of the tile
+  const int warps = (vr + 31) / 32;               // softmax warps that hold any
+
+  const uint32_t sQ = base, sK = base + S::kOffK, sV = base + S::kOffV;
+  const uint32_t bar0 = base + S::kOffBar;
+  const uint32_t bQFull = bar0, bK0 = bar0 + 8u, bV0 = bK0 + 8u * kKS, bS0 = bV0 + 8u * kVS, bP0 = bS0 + 16u,
+                 bO0 = bP0 + 16u, bDrain = bO0 + 8u * kVS;
+  auto bKFull = [&](int c) { return bK0 + 8u * (c % kKS); };
+  auto bVFull = [&](int c) { return bV0 + 8u * (c % kVS); };
+  auto bSFull = [&](int c) { return bS0 + 8u * (c & 1); };
+  auto bPFull = [&](int c) { return bP0 + 8u * (c & 1); };
+  auto bODone = [&](int c) { return bO0 + 8u * (c % kVS); };
+  auto parK = [](int c) { return uint32_t(c / kKS) & 1u; };
+  auto parV = [](int c) { return uint32_t(c / kVS) & 1u; };
+  auto parS = [](int c) { return uint32_t(c >> 1) & 1u; };
+  volatile uint32_t* tmem_holder = reinterpret_cast<volatile uint32_t*>(smem + S::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kOffMisc + 4);
+  volatile int* s_flag = reinterpret_cast<volatile int*>(smem + S::kOffMisc + 8);
+  Run* s_run = reinterpret_cast<Run*>(smem + S::kOffRun);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Ctl ctl{abort_flag, p.status, kWaitNs};
+
+  if constexpr (TREE) {
+    // a later layout row has rows only if the tree is deep enough to reach it
+    if (grp > 0) {
+      const int len = p.lengths[b];
+      const int need = (len / BLK + grp) * BLK - len;
+      if (len < 0 || len > p.n || need > p.T - 1) return;
+      const int most = deepest(p.parents + size_t(b) * p.T, p.T, reinterpret_cast<volatile int8_t*>(smem + S::kOffJump),
+                               reinterpret_cast<volatile int8_t*>(smem + S::kOffDepth),
+                               reinterpret_cast<int*>(smem + S::kOffMisc + 12));
+      if (need > most) return;
+    }
+  }
+  if (threadIdx.x == 0) {
+    Run r{};
+    const int t = p.lengths[b];
+    const int ctx = TREE ? t : t + 1;             // cached keys that exist
+    const int row = TREE ? t / BLK + grp : t / BLK;
+    if ((TREE ? t >= 0 && t <= p.n : t >= 0 && t < p.n) && row < p.nb) {
+      const size_t at = size_t(f0 % p.L) * p.nb + row;
+      r.start = p.row_ptr[at];
+      int len = p.row_ptr[at + 1] - r.start, col = 0;
+      while (len > 0 && (col = p.col_idx[r.start + len - 1]) * BLK >= ctx) --len;   // at most groups + 1 steps
+      if (len > 0) {
+        const int rem = min(BLK, ctx - col * BLK);
+        const int in_last = (rem + kChunk - 1) / kChunk;
+        const int chunks = (len - 1) * CPB + in_last;
+        r.last = chunks - 1;
+        r.tail = rem - (in_last - 1) * kChunk;
+        r.c0 = int(int64_t(chunks) * run / p.S);
+        r.c1 = int(int64_t(chunks) * (run + 1) / p.S);
+      }
+      r.go = 1;
+    }
+    *s_run = r;
+    *s_flag = 0;
+    mbar_init(bQFull, 1);
+    for (int s = 0; s < kKS; ++s) mbar_init(bK0 + 8u * s, 1);
+    for (int s = 0; s < kVS; ++s) mbar_init(bV0 + 8u * s, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bS0 + 8u * s, 1);
+      mbar_init(bP0 + 8u * s, 32 * warps);
+    }
+    for (int s = 0; s < kVS; ++s) mbar_init(bO0 + 8u * s, 1);
+    mbar_init(bDrain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  const Run r = *s_run;
+  const int nch = r.c1 - r.c0;
+  const size_t part = (size_t(unit) * p.S + run) * p.cap;
+  if (nch <= 0) {
+    // an empty run: l = 0 tells kernel 2 that its O was not written
+    if (r.go) {
+      for (int x = threadIdx.x; x < vr; x += kThreads) p.part_ml[part + x] = make_float2(-INFINITY, 0.f);
+      if (threadIdx.x == 0) p.part_flag[size_t(unit) * p.S + run] = 0;
+    }
+    return;
+  }
+  if (warp == 1) {
+    tmem_alloc(base + S::kOffMisc, S::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+
+  if (warp == 0) {
+    // ================================================================ loads
+    if (lane == 0) {
+      mbar_expect_tx(bQFull, S::kQBytes);
+      if constexpr (HD == 128) tma_load_4d(sQ, &tmQ, bQFull, 0, mt * kTileM, 0, bh);
+      else tma_load_3d(sQ, &tmQ, bQFull, 0, mt * kTileM, bh);
+    }
+    const int e0 = r.c0 / CPB, e1 = (r.c1 - 1) / CPB + 1;   // list entries of the run
+    int have = e0, page_of = 0, flag = 0;                   // lane x holds the page of entry have + x
+    auto fetch = [&](int first) {
+      have = first;
+      const int e = first + lane;
+      page_of = 0;
+      if (e < e1) {
+        const int pg = p.page_table[size_t(b) * p.max_blocks + p.col_idx[r.start + e]];
+        if (pg >= 0 && pg < p.num_pages) page_of = pg;
+        else flag = 1;                   // page 0 is read in its place and the rows are refused
+      }
+    };
+    fetch(e0);
+    int kc = 0, vc = 0;
+    auto page_at = [&](int q) -> int {
+      const int e = (r.c0 + q) / CPB;
+      if (e - have >= 32) fetch(e);
+      return __shfl_sync(0xffffffffu, page_of, e - have);
+    };
+    auto load_k = [&](int q, int page) -> bool {
+      if (q >= kKS && !__all_sync(0xffffffffu, ctl.wait(bSFull(q), parS(q - kKS)))) return false;
+      if (lane == 0) {
+        mbar_expect_tx(bKFull(q), S::kTileBytes);
+        tma_load_kv<HD>(sK + (q % kKS) * S::kTileBytes, &tmK, bKFull(q), ((r.c0 + q) % CPB) * kChunk,
+                        page * p.hkv + hk);
+      }
+      ++kc;
+      return true;
+    };
+    auto load_v = [&](int q, int page) -> bool {
+      if (q >= kVS && !__all_sync(0xffffffffu, ctl.wait(bODone(q), parV(q - kVS)))) return false;
+      if (lane == 0) {
+        mbar_expect_tx(bVFull(q), S::kTileBytes);
+        tma_load_kv<HD>(sV + (q % kVS) * S::kTileBytes, &tmV, bVFull(q), ((r.c0 + q) % CPB) * kChunk,
+                        page * p.hkv + hk);
+      }
+      ++vc;
+      return true;
+    };
+    int page = page_at(0);
+    bool ok = load_k(0, page);
+    for (int q = 0; q < nch && ok; ++q) {
+      const int next = q + 1 < nch ? page_at(q + 1) : 0;
+      if (q + 1 < nch) ok = load_k(q + 1, next);
+      if (ok) ok = load_v(q, page);
+      page = next;
+    }
+    if (__any_sync(0xffffffffu, flag) && lane == 0) *s_flag = 1;
+    // never leave the CTA with copies in flight into its shared memory
+    if (lane == 0) {
+      wait_drain(bQFull, 0, kDrainNs);
+      for (int c = max(0, kc - kKS); c < kc; ++c) wait_drain(bKFull(c), parK(c), kDrainNs);
+      for (int c = max(0, vc - kVS); c < vc; ++c) wait_drain(bVFull(c), parV(c), kDrainNs);
+    }
+  } else if (warp == 1) {
+    // ================================================================ products
+    if (lane == 0) {
+      constexpr uint64_t kFixK = sw128_fixed(16, 1024), kFixV = sw128_fixed(S::kAtomKV, 1024);
+      const uint32_t q_lo = uint32_t(kFixK) + (sQ >> 4), k_lo = uint32_t(kFixK) + (sK >> 4);
+      const uint32_t v_lo = uint32_t(kFixV) + (sV >> 4);
+      constexpr uint32_t kHiK = uint32_t(kFixK >> 32), kHiV = uint32_t(kFixV >> 32);
+      auto issue_qk = [&](int c) -> bool {
+        if (!ctl.wait(bKFull(c), parK(c))) return false;
+        tc_fence_after();
+        const uint32_t d = tmem + S::kColS + (c & 1) * kChunk;
+        const uint32_t kb = k_lo + uint32_t(c % kKS) * (S::kTileBytes >> 4);
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk)
+          mma_ss(d, desc_from(q_lo + ((kk >> 2) * S::kAtomQ + (kk & 3) * 32) / 16, kHiK),
+                 desc_from(kb + ((kk >> 2) * S::kAtomKV + (kk & 3) * 32) / 16, kHiK), S::kIdescQK, kk > 0 ? 1u : 0u);
+        tc_commit(bSFull(c));
+        return true;
+      };
+      auto issue_pv = [&](int c) -> bool {
+        if (!ctl.wait(bVFull(c), parV(c))) return false;
+        if (!ctl.wait(bPFull(c), parS(c))) return false;
+        tc_fence_after();
+        const uint32_t pa = tmem + S::kColS + (c & 1) * kChunk;
+        const uint32_t vb = v_lo + uint32_t(c % kVS) * (S::kTileBytes >> 4);
+#pragma unroll
+        for (int part2 = 0; part2 < 2; ++part2)          // P rounded, then the rest of it
+#pragma unroll
+          for (int kk = 0; kk < kChunk / 16; ++kk)
+            mma_ts(tmem + S::kColO, pa + part2 * 32 + kk * 8, desc_from(vb + kk * 16 * 128 / 16, kHiV), S::kIdescPV,
+                   (c > 0 || part2 > 0 || kk > 0) ? 1u : 0u);
+        tc_commit(bODone(c));
+        return true;
+      };
+      bool ok = ctl.wait(bQFull, 0);
+      tc_fence_after();
+      if (ok) ok = issue_qk(0);
+      for (int c = 0; c < nch && ok; ++c) {
+        if (c + 1 < nch) ok = issue_qk(c + 1);
+        if (ok) ok = issue_pv(c);
+      }
+      tc_commit(bDrain);
+      wait_drain(bDrain, 0, kDrainNs);
+    }
+  } else if ((warp & 3) < warps) {
+    // ================================================================ softmax, one row per thread
+    const int q4 = warp & 3;
+    const int row = q4 * 32 + lane;
+    const bool mine = row < vr;
+    const uint32_t lane_base = tmem + (uint32_t(q4 * 32) << 16);
+    const float sl2 = p.scale_log2;
+    float m2 = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int c = 0; c < nch; ++c) {
+      ok = __all_sync(0xffffffffu, ctl.wait(bSFull(c), parS(c)));
+      if (!ok) break;
+      tc_fence_after();
+      float sv[kChunk];
+      const uint32_t s_col = lane_base + S::kColS + (c & 1) * kChunk;
+      tmem_ld32(s_col, sv);
+      tmem_ld32(s_col + 32, sv + 32);
+      tmem_wait_ld();
+      const bool ends = r.c0 + c == r.last && r.tail < kChunk;
+      if (ends) {
+#pragma unroll
+        for (int x = 0; x < kChunk; ++x)
+          if (x >= r.tail) sv[x] = -INFINITY;
+      }
+      if constexpr (!TREE) {
+        if (mine) {
+          float4* to = reinterpret_cast<float4*>(p.scores + size_t(f0 + mt * kTileM + row) * p.score_stride +
+                                                 size_t(r.c0 + c) * kChunk);
+#pragma unroll
+          for (int x = 0; x < kChunk; x += 4) to[x / 4] = make_float4(sv[x], sv[x + 1], sv[x + 2], sv[x + 3]);
+        }
+      }
+      float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < kChunk; x += 4) {
+        mx0 = max3(mx0, sv[x], sv[x + 1]);
+        mx1 = max3(mx1, sv[x + 2], sv[x + 3]);
+      }
+      const float mb = fmaxf(mx0, mx1) * sl2;
+      // the row moves its max only by more than 2^8; -inf (no finite score yet) always moves
+      float alpha = 1.f;
+      const bool need = mb > m2 + kRescaleThreshold;
+      if (need) {
+        alpha = ex2(m2 - mb);
+        m2 = mb;
+      }
+      const float neg_m = m2 == -INFINITY ? 0.f : -m2;
+      float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+      for (int x = 0; x < kChunk; x += 4) {
+        sv[x] = ex2(fmaf(sv[x], sl2, neg_m));
+        sv[x + 1] = ex2(fmaf(sv[x + 1], sl2, neg_m));
+        sv[x + 2] = ex2(fmaf(sv[x + 2], sl2, neg_m));
+        sv[x + 3] = ex2(fmaf(sv[x + 3], sl2, neg_m));
+        s0 += sv[x];
+        s1 += sv[x + 1];
+        s2 += sv[x + 2];
+        s3 += sv[x + 3];
+      }
+      l = l * alpha + ((s0 + s1) + (s2 + s3));
+      if (c > 0 && __any_sync(0xffffffffu, need && mine)) {
+        ok = __all_sync(0xffffffffu, ctl.wait(bODone(c - 1), parV(c - 1)));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int x = 0; x < HD / 32; ++x) {
+          float ov[32];
+          tmem_ld32(lane_base + S::kColO + x * 32, ov);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ov[e] *= alpha;
+          tmem_st32(lane_base + S::kColO + x * 32, ov);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < kChunk / 32; ++x) {
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint32_t a = __float_as_uint(sv[x * 32 + 2 * e]), bb = __float_as_uint(sv[x * 32 + 2 * e + 1]);
+          hi[e] = __byte_perm(a, bb, 0x7632);
+          lo[e] = pack_bf16(rest_of(a), rest_of(bb));
+        }
+        tmem_st16(s_col + x * 16, hi);
+        tmem_st16(s_col + 32 + x * 16, lo);
+      }
+      tmem_wait_st();
+      if (ends) {
+        // Values behind the cached tokens are whatever the page holds, and
+        // 0 * NaN is NaN: they are cleared before the product reads them.
+        ok = __all_sync(0xffffffffu, ctl.wait(bVFull(c), parV(c)));
+        if (!ok) break;
+        const uint32_t v0 = sV + (c % kVS) * S::kTileBytes;
+        const int total = (kChunk - r.tail) * (HD / 8);
+        for (int x = row; x < total; x += 32 * warps) {
+          const int key = r.tail + x / (HD / 8), piece = x % (HD / 8);
+          st_shared_v4(v0 + (piece >> 3) * S::kAtomKV + key * 128 + (piece & 7) * 16, 0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async();
+      }
+      tc_fence_before();
+      mbar_arrive(bPFull(c));
+    }
+    if (ok) ok = __all_sync(0xffffffffu, ctl.wait(bODone(nch - 1), parV(nch - 1)));
+    if (ok) {
+      tc_fence_after();
+      float4* to = reinterpret_cast<float4*>(p.part_o + (part + row) * HD);
+#pragma unroll
+      for (int x = 0; x < HD / 32; ++x) {
+        float ov[32];
+        tmem_ld32(lane_base + S::kColO + x * 32, ov);
+        tmem_wait_ld();
+        if (mine) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) to[x * 8 + e / 4] = make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+        }
+      }
+    }
+    if (mine) p.part_ml[part + row] = make_float2(m2, l);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::kTmemCols);
+  }
+  // 1: a page was out of range, 2: a wait ran out (the partial result is not whole)
+  if (threadIdx.x == 0) p.part_flag[size_t(unit) * p.S + run] = *s_flag | (*abort_flag ? 2 : 0);
+}
+
+// ------------------------------------------------------------ kernel 2
+
+constexpr int kJoinWarps = 8;
+
+// The runs of one row joined: M, L and, per lane, HD / 32 columns of O.
+template <int HD>
+__device__ __forceinline__ int join_runs(const Params& p, int unit, int row, float& M, float& L, float* acc) {
+  const int lane = threadIdx.x & 31;
+  constexpr int DPL = HD / 32;
+  int flag = 0;
+  M = -INFINITY;
+  for (int s = lane; s < p.S; s += 32) {
+    flag |= p.part_flag[size_t(unit) * p.S + s];
+    const float2 ml = p.part_ml[(size_t(unit) * p.S + s) * p.cap + row];
+    if (ml.y != 0.f) M = fmaxf(M, ml.x);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  flag = __reduce_or_sync(0xffffffffu, flag);
+  L = 0.f;
+#pragma unroll
+  for (int e = 0; e < DPL; ++e) acc[e] = 0.f;
+  for (int s0 = 0; s0 < p.S; s0 += 32) {
+    const int s = s0 + lane;
+    float w = 0.f;                       // this lane's run's weight
+    if (s < p.S) {
+      const float2 ml = p.part_ml[(size_t(unit) * p.S + s) * p.cap + row];
+      if (ml.y != 0.f) {
+        w = M == -INFINITY ? 1.f : ex2(ml.x - M);
+        L += w * ml.y;
+      }
+    }
+    const unsigned live = __ballot_sync(0xffffffffu, w != 0.f);
+    const int n = min(32, p.S - s0);
+#pragma unroll 4
+    for (int x = 0; x < n; ++x) {
+      const float wx = __shfl_sync(0xffffffffu, w, x);
+      if (!(live >> x & 1u)) continue;
+      const float* src = p.part_o + ((size_t(unit) * p.S + s0 + x) * p.cap + row) * HD + lane * DPL;
+      if constexpr (DPL == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        acc[0] += wx * v.x;
+        acc[1] += wx * v.y;
+        acc[2] += wx * v.z;
+        acc[3] += wx * v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        acc[0] += wx * v.x;
+        acc[1] += wx * v.y;
+      }
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+  return flag;
+}
+
+template <int HD>
+__device__ __forceinline__ void store_row(const Params& p, size_t row, bool refuse, float M, float L, const float* acc) {
+  const int lane = threadIdx.x & 31;
+  constexpr int DPL = HD / 32;
+  const bool none = refuse || L == 0.f;
+  float v[DPL];
+#pragma unroll
+  for (int e = 0; e < DPL; ++e) v[e] = none ? 0.f : acc[e] / L;
+  uint32_t* to = reinterpret_cast<uint32_t*>(p.o + row * HD + lane * DPL);
+  if constexpr (DPL == 4) *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+  else *to = pack_bf16(v[0], v[1]);
+  if (lane == 0) p.lse[row] = none ? -INFINITY : (M + __log2f(L)) * kLn2;
+}
+
+// Does row `at` of the layout keep block j?
+__device__ __forceinline__ int find_block(const Params& p, size_t at, int j) {
+  int lo = p.row_ptr[at], hi = p.row_ptr[at + 1];
+  const int first = lo;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (p.col_idx[mid] < j) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo < p.row_ptr[at + 1] && p.col_idx[lo] == j ? lo - first : -1;
+}
+
+// The step: blocks [0, row_blocks) join one row per warp; the others turn
+// the scores of 256 list keys of a key/value head into weights.
+template <int BLK, int HD>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_step_kernel(const Params p, int heads, int row_blocks) {
+  __shared__ float s_m[32], s_l[32];
+  __shared__ int s_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_wait();
+  if (int(blockIdx.x) < row_blocks) {
+    const int f = blockIdx.x * kJoinWarps + warp;
+    if (f >= heads) return;
+    const int b = f / p.H, t = p.lengths[b];
+    const bool in = t >= 0 && t < p.n;
+    float M = -INFINITY, L = 0.f, acc[HD / 32] = {};
+    int flag = 0;
+    if (in) {
+      const int hh = f - b * p.H;
+      const int unit = (b * p.hg + hh / p.hpt) * p.mtiles + hh % p.hpt / kTileM;
+      flag = join_runs<HD>(p, unit, hh % p.hpt % kTileM, M, L, acc);
+    }
+    store_row<HD>(p, f, !in || flag, M, L, acc);
+    if (lane == 0 && (!in || (flag & 1))) atomicOr(p.status, kStatusBadIndex);
+    return;
+  }
+  // ---- weights.  With one route for all heads a block takes 256 list keys of
+  // a key/value head and sums its query heads; with a route per head it takes
+  // 256 list keys of one query head, and of the key blocks that several heads
+  // of the group keep each is summed by the first of them.
+  const int x = blockIdx.x - row_blocks;
+  const int tile = x % p.tiles, hg = x / p.tiles;           // hg over batch * head groups
+  const int g = p.H / p.hkv;
+  const int b = hg / p.hg, h0 = (hg - b * p.hg) * p.hpt;    // the block's query head(s) in the sequence
+  const int t = p.lengths[b];
+  if (t < 0 || t >= p.n) return;
+  const size_t at0 = size_t((b * p.H + h0) % p.L) * p.nb + t / BLK;
+  const int list = (p.row_ptr[at0 + 1] - p.row_ptr[at0]) * BLK;
+  if (tile * 256 >= list) return;
+  const int kv = h0 / g, first = p.L == 1 ? h0 : kv * g;    // first query head of the group
+  const int k0 = tile * 256 + threadIdx.x;
+  const int j = k0 < list ? p.col_idx[p.row_ptr[at0] + k0 / BLK] : -1;
+  const int u = j * BLK + k0 % BLK;
+  bool mine = j >= 0 && u <= t;
+  float sum = 0.f;
+  // up to 32 query heads of the group at a time: their M and L, then their scores
+  for (int h1 = 0; h1 < g; h1 += 32) {
+    const int count = min(32, g - h1);
+    __syncthreads();
+    if (threadIdx.x == 0) s_flag = 0;
+    __syncthreads();
+    for (int h = warp; h < count; h += kJoinWarps) {
+      const int hh = first + h1 + h;
+      const int unit = (b * p.hg + hh / p.hpt) * p.mtiles + hh % p.hpt / kTileM, row = hh % p.hpt % kTileM;
+      float M = -INFINITY, L = 0.f;
+      int flag = 0;
+      for (int s = lane; s < p.S; s += 32) {
+        flag |= p.part_flag[size_t(unit) * p.S + s];
+        const float2 ml = p.part_ml[(size_t(unit) * p.S + s) * p.cap + row];
+        if (ml.y != 0.f) M = fmaxf(M, ml.x);
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+      for (int s = lane; s < p.S; s += 32) {
+        const float2 ml = p.part_ml[(size_t(unit) * p.S + s) * p.cap + row];
+        if (ml.y != 0.f) L += (M == -INFINITY ? 1.f : ex2(ml.x - M)) * ml.y;
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+      if (lane == 0) {
+        s_m[h] = M;
+        s_l[h] = L;
+      }
+      flag = __reduce_or_sync(0xffffffffu, flag);
+      if (lane == 0 && flag) atomicOr(&s_flag, 1 << h);
+    }
+    __syncthreads();
+    if (mine) {
+      for (int h = 0; h < count; ++h) {
+        const int hh = first + h1 + h;
+        int k = k0;
+        if (p.L > 1 && hh != h0) {
+          const int e = find_block(p, size_t((b * p.H + hh) % p.L) * p.nb + t / BLK, j);
+          if (e < 0) continue;
+          if (hh < h0) {                 // an earlier head of the group keeps the block and sums it
+            mine = false;
+            break;
+          }
+          k = e * BLK + k0 % BLK;
+        }
+        // a refused row and a row without any weight add nothing
+        if ((s_flag >> h & 1) || s_l[h] == 0.f) continue;
+        const float s = p.scores[size_t(b * p.H + hh) * p.score_stride + k];
+        const float m = s_m[h];
+        sum += ex2(fmaf(s, p.scale_log2, m == -INFINITY ? 0.f : -m)) / s_l[h];
+      }
+    }
+  }
+  if (mine) p.weights[size_t(b * p.hkv + kv) * p.weights_stride + u] += sum;
+}
+
+// The tree: one row (query head, drafted token) per warp, its runs joined with
+// its ancestors' keys.
+template <int BLK, int HD>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_tree_kernel(const Params p) {
+  constexpr int DPL = HD / 32, CPL = HD / 8;
+  __shared__ int s_par[kMaxT];
+  __shared__ int s_path[kJoinWarps][kMaxT];       // ancestors from the token up to its root
+  __shared__ float s_sc[kJoinWarps][kMaxT];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tb = (p.T + kJoinWarps - 1) / kJoinWarps;
+  const int f = blockIdx.x / tb, i = blockIdx.x % tb * kJoinWarps + warp;
+  const int b = f / p.H, hh = f - b * p.H;
+  for (int x = threadIdx.x; x < p.T; x += blockDim.x) s_par[x] = p.parents[size_t(b) * p.T + x];
+  __syncthreads();
+  const int len = p.lengths[b];
+  const bool live = i < p.T && s_par[i] != -2;    // an unused row is left as it was
+  // the path to the root; every parent is an earlier token, so the walk ends
+  int count = 0;
+  bool bad = len < 0 || len > p.n;
+  if (live) {
+    for (int x = i;;) {
+      if (lane == 0) s_path[warp][count] = x;
+      ++count;
+      const int up = s_par[x];
+      if (up == -1) break;
+      if (up < 0 || up >= x) {
+        bad = true;
+        break;
+      }
+      x = up;
+    }
+  }
+  __syncwarp();
+  const int pos = bad ? 0 : len + count - 1;
+  if (pos >= p.n) bad = true;
+  // the layout row of the token, and which of the blocks that its path lies in it keeps
+  const int blk = pos / BLK, blk0 = bad ? 0 : len / BLK;
+  const size_t at = size_t(f % p.L) * p.nb + blk;
+  bool kept = false;
+  if (live && !bad && lane <= blk - blk0) kept = find_block(p, at, blk0 + lane) >= 0;
+  const unsigned keeps = __ballot_sync(0xffffffffu, kept);
+  const int grp = blk - blk0;
+  // scores of the ancestors: 8 lanes a key, four keys at a time
+  const int sub = lane >> 3, pc = lane & 7;
+  const int kvh = b * p.hkv + hh / (p.H / p.hkv);
+  float top = -INFINITY;
+  if (live && !bad) {
+    float qr[CPL];
+    const uint4* qs = reinterpret_cast<const uint4*>(p.q + (size_t(f) * p.T + i) * HD + pc * CPL);
+#pragma unroll
+    for (int c = 0; c < CPL / 8; ++c) {
+      const uint4 w = qs[c];
+      bf16x2_to_f32(w.x, qr[c * 8], qr[c * 8 + 1]);
+      bf16x2_to_f32(w.y, qr[c * 8 + 2], qr[c * 8 + 3]);
+      bf16x2_to_f32(w.z, qr[c * 8 + 4], qr[c * 8 + 5]);
+      bf16x2_to_f32(w.w, qr[c * 8 + 6], qr[c * 8 + 7]);
+    }
+    for (int x0 = 0; x0 < count; x0 += 4) {
+      const int x = x0 + sub;
+      const bool use = x < count && (keeps >> ((len + count - 1 - x) / BLK - blk0) & 1u);
+      float dot = 0.f;
+      if (use) {
+        const uint4* ks = reinterpret_cast<const uint4*>(p.k_tree + (size_t(kvh) * p.T + s_path[warp][x]) * HD + pc * CPL);
+#pragma unroll
+        for (int c = 0; c < CPL / 8; ++c) {
+          const uint4 w = ks[c];
+          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float k0, k1;
+            bf16x2_to_f32(ws[e], k0, k1);
+            dot = fmaf(k0, qr[c * 8 + 2 * e], dot);
+            dot = fmaf(k1, qr[c * 8 + 2 * e + 1], dot);
+          }
+        }
+      }
+      dot += __shfl_xor_sync(0xffffffffu, dot, 1);
+      dot += __shfl_xor_sync(0xffffffffu, dot, 2);
+      dot += __shfl_xor_sync(0xffffffffu, dot, 4);
+      const float s = use ? dot * p.scale_log2 : -INFINITY;
+      if (pc == 0 && x < count) s_sc[warp][x] = s;
+      top = fmaxf(top, s);
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+  }
+  __syncwarp();
+  grid_wait();                                    // the runs of kernel 1 are in memory from here on
+  if (!live) return;
+  float M = -INFINITY, L = 0.f, acc[DPL] = {};
+  int flag = 0;
+  if (!bad) {
+    const int row = hh % p.hpt * p.T + i;
+    const int unit = ((b * p.hg + hh / p.hpt) * p.mtiles + row / kTileM) * p.groups + grp;
+    flag = join_runs<HD>(p, unit, row % kTileM, M, L, acc);
+    // the cache's part and the path's under one max
+    const float all = fmaxf(M, top);
+    const float a = M == -INFINITY ? (L == 0.f ? 0.f : 1.f) : ex2(M - all);
+    L *= a;
+#pragma unroll
+    for (int e = 0; e < DPL; ++e) acc[e] *= a;
+    float sum = 0.f;
+    for (int x = lane; x < count; x += 32) {
+      const float s = s_sc[warp][x];
+      // an ancestor that is not read is marked by NaN-free 0 and skipped below
+      const bool use = keeps >> ((len + count - 1 - x) / BLK - blk0) & 1u;
+      const float w = use ? ex2(s - (all == -INFINITY ? 0.f : all)) : 0.f;
+      s_sc[warp][x] = w;
+      sum += w;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    L += sum;
+    M = all;
+    __syncwarp();
+#pragma unroll 4
+    for (int x = 0; x < count; ++x) {
+      if (!(keeps >> ((len + count - 1 - x) / BLK - blk0) & 1u)) continue;
+      const float w = s_sc[warp][x];
+      const uint32_t* vs = reinterpret_cast<const uint32_t*>(p.v_tree + (size_t(kvh) * p.T + s_path[warp][x]) * HD + lane * DPL);
+#pragma unroll
+      for (int e = 0; e < DPL; e += 2) {
+        float v0, v1;
+        bf16x2_to_f32(vs[e / 2], v0, v1);
+        acc[e] = fmaf(w, v0, acc[e]);
+        acc[e + 1] = fmaf(w, v1, acc[e + 1]);
+      }
+    }
+  }
+  store_row<HD>(p, size_t(f) * p.T + i, bad || flag, M, L, acc);
+  if (lane == 0 && (bad || (flag & 1))) atomicOr(p.status, kStatusBadIndex);
+}
+
+// ------------------------------------------------------------ host side
+
+// Kernel 2 is launched while kernel 1 still runs and waits for its end on the device.
+template <class F, class... A>
+int launch_after(const char* what, F kern, unsigned grid, unsigned threads, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  if (e != cudaSuccess) return set_error(BSA_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+  return BSA_OK;
+}
+
+struct Call {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  int batch, heads, kv_heads;
+  Plan plan;
+  cudaStream_t stream;
+};
+
+template <int BLK, int HD, bool TREE>
+int launch(const Call& c, const Params& p) {
+  using S = Shape<BLK, HD>;
+  auto kern = paged_attention_kernel<BLK, HD, TREE>;
+  // enough shared memory that no third CTA shares an SM: TMEM holds two
+  constexpr int smem = S::kSmem < 77 * 1024 ? 77 * 1024 : S::kSmem;
+  static_assert(2 * (smem + 1024) <= 228 * 1024, "two CTAs per SM");
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= 64) return set_error(BSA_ERR_CUDA, "cannot query the device");
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev]) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return set_error(BSA_ERR_CUDA, std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e));
+      done[dev] = true;
+    }
+  }
+  CUtensorMap mq, mk, mv;
+  int st = tmap::encode_rows(&mq, c.q, c.batch * c.plan.hg, c.plan.rows, HD, kTileM);
+  if (st == BSA_OK) st = tmap::encode_rows(&mk, c.k_cache, p.num_pages * p.hkv, BLK, HD, kChunk);
+  if (st == BSA_OK) st = tmap::encode_rows(&mv, c.v_cache, p.num_pages * p.hkv, BLK, HD, kChunk);
+  if (st != BSA_OK) return st;
+  kern<<<unsigned(c.plan.units) * unsigned(c.plan.S), kThreads, smem, c.stream>>>(mq, mk, mv, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return set_error(BSA_ERR_CUDA, std::string("paged attention launch: ") + cudaGetErrorString(e));
+  if constexpr (TREE) {
+    const unsigned tb = unsigned(p.T + kJoinWarps - 1) / kJoinWarps;
+    return launch_after("tree join launch", join_tree_kernel<BLK, HD>, unsigned(c.heads) * tb, kJoinWarps * 32, c.stream, p);
+  } else {
+    const int row_blocks = (c.heads + kJoinWarps - 1) / kJoinWarps;
+    const unsigned grid = unsigned(row_blocks) + unsigned(c.batch * c.plan.hg) * unsigned(p.tiles);
+    return launch_after("step join launch", join_step_kernel<BLK, HD>, grid, kJoinWarps * 32, c.stream, p, c.heads,
+                        row_blocks);
+  }
+}
+
+bool aligned(const void* x, uintptr_t a) { return (reinterpret_cast<uintptr_t>(x) % a) == 0; }
+
+// What both entry points check of the sizes; workspace sizes are 0 where it fails.
+int check_sizes(const bsa_layout* layout, int batch, int heads, int kv_heads, int T, int d) {
+  if (!layout) return set_error(BSA_ERR_INVALID_ARG, "layout is NULL");
+  if (layout->B != 64 && layout->B != 128) return set_error(BSA_ERR_UNSUPPORTED, "B must be 64 or 128");
+  if (d != 64 && d != 128) return set_error(BSA_ERR_UNSUPPORTED, "d must be 64 or 128");
+  if (batch < 1 || heads < 1 || kv_heads < 1) return set_error(BSA_ERR_SHAPE, "batch, heads and kv_heads must be >= 1");
+  if (heads % batch || kv_heads % batch)
+    return set_error(BSA_ERR_SHAPE, "heads and kv_heads must be multiples of batch");
+  const int H = heads / batch, hkv = kv_heads / batch;
+  if (H % hkv) return set_error(BSA_ERR_SHAPE, "query heads per sequence must be a multiple of its kv heads");
+  if (H % layout->L) return set_error(BSA_ERR_SHAPE, "query heads per sequence must be a multiple of layout_heads");
+  if (T < 1 || T > kMaxT) return set_error(BSA_ERR_UNSUPPORTED, "the tree must have 1 to 128 tokens");
+  if (int64_t(H / hkv) * T > INT32_MAX / 2) return set_error(BSA_ERR_SHAPE, "too many query rows");
+  const Plan p = plan_of(layout, batch, heads, kv_heads, T);
+  if (int64_t(p.units) * p.S > INT32_MAX || int64_t(heads) * ((T + kJoinWarps - 1) / kJoinWarps) > INT32_MAX / 2)
+    return set_error(BSA_ERR_SHAPE, "too many query rows");
+  return BSA_OK;
+}
+
+int check_call(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table, int max_blocks,
+               int num_pages, const int32_t* lengths, const bsa_layout* layout, int batch, int heads, int kv_heads,
+               int T, int d, float scale, const void* o, const float* lse) {
+  if (!layout) return set_error(BSA_ERR_INVALID_ARG, "layout is NULL");
+  const int st = check_sizes(layout, batch, heads, kv_heads, T, d);
+  if (st != BSA_OK) return st;
+  if (max_blocks < layout->nb) return set_error(BSA_ERR_SHAPE, "max_blocks is smaller than the layout's blocks");
+  if (num_pages < 1 || int64_t(num_pages) * (kv_heads / batch) > INT32_MAX)
+    return set_error(BSA_ERR_SHAPE, "num_pages must be >= 1 and num_pages * kv heads below 2^31");
+  if (!(std::isfinite(scale) && scale > 0.f)) return set_error(BSA_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (!q || !k_cache || !v_cache || !page_table || !lengths || !o || !lse)
+    return set_error(BSA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16))
+    return set_error(BSA_ERR_INVALID_ARG, "q, k_cache, v_cache and o must be 16-byte aligned");
+  if (!aligned(lse, 4) || !aligned(page_table, 4) || !aligned(lengths, 4))
+    return set_error(BSA_ERR_INVALID_ARG, "lse, page_table and positions or lengths must be 4-byte aligned");
+  return BSA_OK;
+}
+
+int run(bool tree, const void* q, const void* k_tree, const void* v_tree, const void* k_cache, const void* v_cache,
+        const int32_t* page_table, int max_blocks, int num_pages, const int32_t* lengths, const int32_t* parents,
+        const bsa_layout* layout, int T, int batch, int heads, int kv_heads, int d, float scale, void* o, float* lse,
+        float* weights, size_t weights_stride, void* workspace, size_t workspace_bytes, void* stream) {
+  const Plan pl = plan_of(layout, batch, heads, kv_heads, T);
+  const Offsets of = offsets_of(pl, layout, heads, d, !tree);
+  if (!workspace || !aligned(workspace, 16))
+    return set_error(BSA_ERR_INVALID_ARG, "workspace must be non-null and 16-byte aligned");
+  if (workspace_bytes < of.total)
+    return set_error(BSA_ERR_SHAPE, "workspace too small: " + std::to_string(of.total) + " bytes needed");
+  int st = check_layout_device(layout);
+  if (st == BSA_OK) st = tmap::get_encoder();
+  if (st != BSA_OK) return st;
+  char* w = static_cast<char*>(workspace);
+  Params p{};
+  p.page_table = page_table;
+  p.lengths = lengths;
+  p.parents = parents;
+  p.row_ptr = layout->d_row_ptr;
+  p.col_idx = layout->d_col_idx;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_tree = static_cast<const __nv_bfloat16*>(k_tree);
+  p.v_tree = static_cast<const __nv_bfloat16*>(v_tree);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.weights = weights;
+  p.weights_stride = weights_stride;
+  p.part_o = reinterpret_cast<float*>(w);
+  p.part_ml = reinterpret_cast<float2*>(w + of.ml);
+  p.part_flag = reinterpret_cast<int*>(w + of.flag);
+  p.scores = reinterpret_cast<float*>(w + of.scores);
+  p.score_stride = size_t(layout->max_row) * layout->B;
+  p.status = layout->d_status;
+  p.n = layout->n;
+  p.nb = layout->nb;
+  p.L = layout->L;
+  p.H = heads / batch;
+  p.hkv = kv_heads / batch;
+  p.max_blocks = max_blocks;
+  p.num_pages = num_pages;
+  p.max_row = layout->max_row;
+  p.hg = pl.hg;
+  p.hpt = pl.hpt;
+  p.rows = pl.rows;
+  p.mtiles = pl.mtiles;
+  p.groups = pl.groups;
+  p.S = pl.S;
+  p.cap = pl.cap;
+  p.T = T;
+  p.tiles = std::max(1, (layout->max_row * layout->B + 255) / 256);
+  p.scale_log2 = float(double(scale) * 1.4426950408889634);
+  const Call c{q, k_cache, v_cache, batch, heads, kv_heads, pl, static_cast<cudaStream_t>(stream)};
+  const int B = layout->B;
+  if (tree) {
+    if (B == 64) return d == 128 ? launch<64, 128, true>(c, p) : launch<64, 64, true>(c, p);
+    return d == 128 ? launch<128, 128, true>(c, p) : launch<128, 64, true>(c, p);
+  }
+  if (B == 64) return d == 128 ? launch<64, 128, false>(c, p) : launch<64, 64, false>(c, p);
+  return d == 128 ? launch<128, 128, false>(c, p) : launch<128, 64, false>(c, p);
+}
+
+}  // namespace paged
+}  // namespace bsa
+
+extern "C" {
+
+size_t bsa_decode_weights_workspace_bytes(const bsa_layout* layout, int batch, int heads, int kv_heads, int d) {
+  using namespace bsa::paged;
+  if (check_sizes(layout, batch, heads, kv_heads, 1, d) != BSA_OK) return 0;
+  return offsets_of(plan_of(layout, batch, heads, kv_heads, 1), layout, heads, d, true).total;
+}
+
+size_t bsa_decode_tree_workspace_bytes(const bsa_layout* layout, int batch, int heads, int kv_heads, int T, int d) {
+  using namespace bsa::paged;
+  if (check_sizes(layout, batch, heads, kv_heads, T, d) != BSA_OK) return 0;
+  return offsets_of(plan_of(layout, batch, heads, kv_heads, T), layout, heads, d, false).total;
+}
+
+int bsa_decode_weights(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
+                       int max_blocks, int num_pages, const int32_t* positions, const bsa_layout* layout, int batch,
+                       int heads, int kv_heads, int d, float scale, void* o, float* lse, float* weights,
+                       size_t weights_stride, void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace bsa;
+  const int st = paged::check_call(q, k_cache, v_cache, page_table, max_blocks, num_pages, positions, layout, batch,
+                                   heads, kv_heads, 1, d, scale, o, lse);
+  if (st != BSA_OK) return st;
+  if (!weights || !paged::aligned(weights, 4))
+    return set_error(BSA_ERR_INVALID_ARG, "weights must be non-null and 4-byte aligned");
+  if (weights_stride < size_t(layout->n)) return set_error(BSA_ERR_SHAPE, "weights_stride is smaller than the layout's n");
+  return paged::run(false, q, nullptr, nullptr, k_cache, v_cache, page_table, max_blocks, num_pages, positions, nullptr,
+                    layout, 1, batch, heads, kv_heads, d, scale, o, lse, weights, weights_stride, workspace,
+                    workspace_bytes, stream);
+}
+
+int bsa_decode_tree(const void* q, const void* k_tree, const void* v_tree, const void* k_cache, const void* v_cache,
+                    const int32_t* page_table, int max_blocks, int num_pages, const int32_t* lengths,
+                    const int32_t* parents, const bsa_layout* layout, int T, int batch, int heads, int kv_heads, int d,
+                    float scale, void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace bsa;
+  const int st = paged::check_call(q, k_cache, v_cache, page_table, max_blocks, num_pages, lengths, layout, batch, heads,
+                                   kv_heads, T, d, scale, o, lse);
+  if (st != BSA_OK) return st;
+  if (!k_tree || !v_tree || !parents) return set_error(BSA_ERR_INVALID_ARG, "null pointer");
+  if (!paged::aligned(k_tree, 16) || !paged::aligned(v_tree, 16))
+    return set_error(BSA_ERR_INVALID_ARG, "k_tree and v_tree must be 16-byte aligned");
+  if (!paged::aligned(parents, 4)) return set_error(BSA_ERR_INVALID_ARG, "parents must be 4-byte aligned");
+  return paged::run(true, q, k_tree, v_tree, k_cache, v_cache, page_table, max_blocks, num_pages, lengths, parents,
+                    layout, T, batch, heads, kv_heads, d, scale, o, lse, nullptr, 0, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -1,7 +1,8 @@
 /*
  * bsa.h -- C ABI of the B200 (sm_100a) block-sparse causal attention
- * forward, its gradients, selected-page decode and BSBR's between-chunk
- * retrieval term.
+ * forward, its gradients, selected-page decode, attention of drafted token
+ * trees, cache eviction by attention weight and BSBR's between-chunk retrieval
+ * term.
  *
  * What the library computes ("Block-Sparse Attention", ai-model-reference,
  * sections "How It Works" and "Math Or Compute Schema"): the sequence of n
@@ -264,6 +265,145 @@ int bsa_decode(const void* q, const void* k_cache, const void* v_cache,
                const int32_t* positions, const bsa_layout* layout, int batch,
                int heads, int kv_heads, int d, float scale, void* o, float* lse,
                void* stream);
+
+/* Bytes of device workspace bsa_attention_weights needs: partial sums of the
+ * column runs of every key block, fp32.  Depends on the layout (a host-only one
+ * will do), not on d.  0 for sizes the call would refuse. */
+size_t bsa_attention_weights_workspace_bytes(const bsa_layout* layout, int heads, int kv_heads);
+
+/* The attention weight that every key of a prompt has received, added to
+ * `weights` (a cache is cut by it, see bsa_evict): for key/value head g and
+ * token u
+ *   weights[g * weights_stride + u] += sum over the query heads f of g and the
+ *       tokens t that may read u (block u / B kept by t's block of layout head
+ *       f % layout_heads, u <= t) of exp(scale <q[f][t], k[g][u]> - lse[f][t]),
+ * lse being bsa_forward's (the sums are then the column sums of the forward's
+ * probabilities).  A row whose lse is -inf adds nothing.  Layouts: q
+ * [heads][n][d] bf16; k [kv_heads][n][d] bf16; lse [heads][n] fp32; weights
+ * fp32, rows weights_stride >= n floats apart, set to zero by the caller
+ * before a prompt's first call.  All sums are fp32 in an order that the layout
+ * fixes, so a call gives the same bits every time.  Requirements (checked
+ * before launch; errors launch nothing): as for bsa_forward; workspace
+ * 16-byte aligned and of at least the bytes above, used by no other call at
+ * the same time.  Enqueues two kernels (none for an explicit mask that keeps
+ * no block) and returns; no allocation. */
+int bsa_attention_weights(const void* q, const void* k, const float* lse,
+                          const bsa_layout* layout, int B, int n, int heads, int kv_heads,
+                          int d, float scale, float* weights, size_t weights_stride,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace bsa_decode_weights needs: the partial softmax
+ * states of its runs and the scores of one step.  0 for sizes the call would
+ * refuse. */
+size_t bsa_decode_weights_workspace_bytes(const bsa_layout* layout, int batch, int heads,
+                                          int kv_heads, int d);
+
+/* A decode step that adds up the weights it gives: o and lse as bsa_decode
+ * gives them (with P rounded nowhere before o), and for every key/value head
+ * kv of sequence b and every cached token u that its query rows read
+ *   weights[(b*Hkv + kv) * weights_stride + u] += sum over the query rows f of
+ *       kv that read u of exp(s_u - lse[f]).
+ * Arguments and layouts as for bsa_decode; weights fp32, rows weights_stride
+ * >= n floats apart (n the layout's).  A refused row (position or page out of
+ * range) adds nothing; weights of tokens that no row reads are not touched.
+ * Requirements as for bsa_decode, and: num_pages * Hkv below 2^31; workspace
+ * 16-byte aligned and of at least the bytes above, used by no other call at
+ * the same time; weights not overlapping any other argument.  The sums' order
+ * is fixed, so a call gives the same bits every time.  Enqueues two kernels
+ * and returns; no allocation. */
+int bsa_decode_weights(const void* q, const void* k_cache, const void* v_cache,
+                       const int32_t* page_table, int max_blocks, int num_pages,
+                       const int32_t* positions, const bsa_layout* layout, int batch,
+                       int heads, int kv_heads, int d, float scale, void* o, float* lse,
+                       float* weights, size_t weights_stride, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace bsa_evict needs: the moves of every key/value
+ * head.  0 for sizes the call would refuse. */
+size_t bsa_evict_workspace_bytes(const bsa_layout* layout, int batch, int kv_heads, int budget);
+
+/* Cut a paged cache to a budget by accumulated weight, in place.  Sequence b
+ * has lengths[b] cached tokens (0 .. n, n the layout's) in the slots
+ * 0 .. lengths[b] - 1 of its pages, slot s being row s % B of page
+ * page_table[b][s / B].  For each key/value head (row r = b*Hkv + kv of
+ * weights and tokens; each head chooses for itself):
+ *   slot s holds token tokens[r*stride + s] (token s when tokens is NULL);
+ *   newest = the largest token of the row (-1 for no tokens);
+ *   if lengths[b] <= budget every token stays, else `budget` of them: first
+ *   those with token > newest - recent, then by weight, the largest first, the
+ *   lower slot at equal weights (a NaN counts as -inf).
+ * With kept = min(lengths[b], budget), a token that stays and lies in a slot
+ * below kept keeps its slot; the i-th of the other slots below kept takes the
+ * i-th token that stays from the slots behind (key and value are copied, both
+ * in slot order).  Then
+ *   weights_out[r*stride + s], tokens_out[r*stride + s] = the weight and token
+ *       now in slot s, for s < kept; 0 and newest + 1 + (s - kept) for
+ *       kept <= s < n, ready for the tokens to come in order;
+ *   lengths_out[b] = kept.
+ * Slots behind kept keep whatever they held: pages past kept tokens may be
+ * freed.  Attention over a cut cache reads it by slots, e.g. bsa_decode with a
+ * layout whose rows keep every block and positions of lengths - 1.
+ * Layouts: caches [num_pages][Hkv][B][d] bf16, written; page_table
+ * [batch][max_blocks], lengths, lengths_out [batch], tokens, tokens_out int32;
+ * weights, weights_out fp32, rows of all four `stride` elements apart.  The
+ * layout supplies the device, B, n and the status word (its kept blocks are
+ * not read).  Requirements (checked before launch; errors launch nothing):
+ * layout on the current device; B in {64, 128}; d in {64, 128}; batch,
+ * kv_heads, budget, num_pages >= 1; kv_heads a multiple of batch;
+ * 0 <= recent <= budget; max_blocks >= the layout's blocks; stride >= n;
+ * pointers (but tokens) non-null, caches and workspace 16-byte aligned, the
+ * rest 4-byte aligned; the outputs must not overlap the inputs, and no page
+ * may stand twice among the pages of the batch's cached tokens; workspace used
+ * by no other call at the same time.  A length outside [0, n], or a page
+ * outside [0, num_pages) among a sequence's cached tokens when it has to be
+ * cut, leaves that sequence's caches, weights_out and tokens_out as they were,
+ * sets lengths_out[b] = -1, and bsa_get_status then reports BSA_ERR_SHAPE.
+ * Enqueues two kernels and returns; no allocation. */
+int bsa_evict(void* k_cache, void* v_cache, const int32_t* page_table, int max_blocks,
+              int num_pages, const int32_t* lengths, const float* weights,
+              const int32_t* tokens, const bsa_layout* layout, int batch, int kv_heads, int d,
+              int budget, int recent, size_t stride, float* weights_out,
+              int32_t* tokens_out, int32_t* lengths_out, void* workspace,
+              size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace bsa_decode_tree needs: the partial softmax states
+ * of its runs.  0 for sizes the call would refuse. */
+size_t bsa_decode_tree_workspace_bytes(const bsa_layout* layout, int batch, int heads,
+                                       int kv_heads, int T, int d);
+
+/* Attention of a tree of T drafted tokens per sequence over its paged cache
+ * and the tokens' own ancestors: one pass that gives every drafted token what
+ * bsa_decode would give it were the path from the root down to it in the
+ * cache.  Sequence b has lengths[b] cached tokens (positions 0 ..
+ * lengths[b] - 1); parents[b*T + i] names drafted token i's parent: an earlier
+ * drafted token (0 .. i - 1), -1 for a token that follows the cache, or -2 for
+ * an unused row, whose o and lse are left as they were.  Token i at depth e
+ * (0 for a parent of -1) has position t = lengths[b] + e, block t / B; query
+ * row (f, i), f = b*H + h, reads of the key blocks that block t / B of layout
+ * head f % layout_heads keeps
+ *   the cached tokens u < lengths[b], and
+ *   itself and its ancestors, each at its own position
+ * with key/value head h / (H / Hkv):  lse[f][i] = ln sum exp(scale <q, k>),
+ * o[f][i] = sum exp(scale <q, k> - lse[f][i]) v; a row with nothing to read
+ * gets o = 0 and lse = -inf.  Layouts: q, o [heads][T][d], k_tree, v_tree
+ * [kv_heads][T][d], caches as for bsa_decode, all bf16; lse [heads][T] fp32;
+ * page_table [batch][max_blocks], lengths [batch], parents [batch][T] int32.
+ * Cached rows at or past lengths[b] are never used, whatever they hold; a key
+ * or value that a row's route or path leaves out has no effect on the row,
+ * infinities and NaN included.  Requirements (checked before launch; errors
+ * launch nothing) as for bsa_decode, and: 1 <= T <= 128; num_pages * Hkv below
+ * 2^31; k_tree and v_tree 16-byte aligned; workspace 16-byte aligned and of at
+ * least the bytes above, used by no other call at the same time.  A length
+ * outside [0, n], a parent outside [-2, i), a parent that is unused or refused,
+ * a position outside [0, n) or a page outside [0, num_pages) is not followed:
+ * the rows it concerns get o = 0, lse = -inf, and bsa_get_status then reports
+ * BSA_ERR_SHAPE.  Enqueues two kernels and returns; no allocation. */
+int bsa_decode_tree(const void* q, const void* k_tree, const void* v_tree,
+                    const void* k_cache, const void* v_cache, const int32_t* page_table,
+                    int max_blocks, int num_pages, const int32_t* lengths,
+                    const int32_t* parents, const bsa_layout* layout, int T, int batch,
+                    int heads, int kv_heads, int d, float scale, void* o, float* lse,
+                    void* workspace, size_t workspace_bytes, void* stream);
 
 /* Gradients of the forward ("BF1: A Causal Dyadic Sparse-Attention Retrofit
  * for Efficient Long-Context Transformers", section 4: the operator is gated

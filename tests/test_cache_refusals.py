@@ -1,0 +1,143 @@
+"""What the cache operators refuse before anything is launched, on the CPU:
+argument checks come before the check of the device, so a host-only layout and
+pointers that are never followed reach every one of them."""
+import ctypes
+
+import pytest
+
+import block_sparse_long_bsa_b200 as bsa
+from oracle import layouts as OL
+
+INVALID, SHAPE, UNSUPPORTED = 1, 2, 3
+N, B = 1000, 64
+P = 1 << 20          # an aligned address that no refused call follows
+
+
+@pytest.fixture(scope="module")
+def lay():
+    from block_sparse_long_bsa_b200 import build
+    build.build()
+    lay = bsa.Layout(OL.DYADIC, N, B, 2, -1, window=2, global_first=1, dyadic_kmin=2)
+    yield lay
+    lay.close()
+
+
+def _status(call, args):
+    with pytest.raises(bsa.BsaError) as e:
+        call(*args.values())
+    return e.value.status
+
+
+def _weights_args(lay, **bad):
+    args = dict(q=P, k=P, lse=P, layout=lay.handle, B=B, n=N, heads=8, kv_heads=4, d=64, scale=0.1, weights=P,
+                stride=N, workspace=P, size=1 << 40)
+    args.update(bad)
+    return args
+
+
+def _step_args(lay, **bad):
+    args = dict(q=P, kc=P, vc=P, table=P, max_blocks=16, num_pages=32, positions=P, layout=lay.handle, batch=2, heads=8,
+                kv_heads=4, d=64, scale=0.1, o=P, lse=P, weights=P, stride=N, workspace=P, size=1 << 40)
+    args.update(bad)
+    return args
+
+
+def _evict_args(lay, **bad):
+    args = dict(kc=P, vc=P, table=P, max_blocks=16, num_pages=32, lengths=P, weights=P, tokens=P, layout=lay.handle,
+                batch=2, kv_heads=4, d=64, budget=100, recent=10, stride=N, weights_out=2 * P, tokens_out=3 * P,
+                lengths_out=4 * P, workspace=P, size=1 << 40)
+    args.update(bad)
+    return args
+
+
+def _tree_args(lay, **bad):
+    args = dict(q=P, kt=P, vt=P, kc=P, vc=P, table=P, max_blocks=16, num_pages=32, lengths=P, parents=P,
+                layout=lay.handle, T=8, batch=2, heads=8, kv_heads=4, d=64, scale=0.1, o=P, lse=P, workspace=P,
+                size=1 << 40)
+    args.update(bad)
+    return args
+
+
+CALLS = {"weights": (bsa.bsa_attention_weights, _weights_args), "step": (bsa.bsa_decode_weights, _step_args),
+         "evict": (bsa.bsa_evict, _evict_args), "tree": (bsa.bsa_decode_tree, _tree_args)}
+
+BAD = [
+    ("weights", dict(B=128), SHAPE), ("weights", dict(n=N - 1), SHAPE), ("weights", dict(stride=N - 1), SHAPE),
+    ("weights", dict(heads=6, kv_heads=4), SHAPE), ("weights", dict(heads=3, kv_heads=1), SHAPE),
+    ("weights", dict(q=P + 8), INVALID), ("weights", dict(weights=P + 2), INVALID), ("weights", dict(lse=0), INVALID),
+    ("step", dict(stride=N - 1), SHAPE), ("step", dict(max_blocks=15), SHAPE), ("step", dict(num_pages=0), SHAPE),
+    ("step", dict(num_pages=(1 << 31) - 1), SHAPE), ("step", dict(positions=0), INVALID),
+    ("step", dict(kc=P + 8), INVALID), ("step", dict(weights=0), INVALID), ("step", dict(heads=7), SHAPE),
+    ("evict", dict(budget=0), SHAPE), ("evict", dict(recent=-1), SHAPE), ("evict", dict(recent=101), SHAPE),
+    ("evict", dict(stride=N - 1), SHAPE), ("evict", dict(max_blocks=15), SHAPE), ("evict", dict(num_pages=0), SHAPE),
+    ("evict", dict(weights_out=P), INVALID), ("evict", dict(tokens_out=P), INVALID),
+    ("evict", dict(lengths_out=P), INVALID), ("evict", dict(kv_heads=3), SHAPE), ("evict", dict(kc=P + 8), INVALID),
+    ("evict", dict(lengths=P + 2), INVALID),
+    ("tree", dict(T=0), UNSUPPORTED), ("tree", dict(T=129), UNSUPPORTED), ("tree", dict(parents=0), INVALID),
+    ("tree", dict(kt=P + 8), INVALID), ("tree", dict(vt=0), INVALID), ("tree", dict(max_blocks=15), SHAPE),
+    ("tree", dict(heads=4, kv_heads=8), SHAPE), ("tree", dict(parents=P + 1), INVALID),
+] + [(name, bad, code) for name in CALLS for bad, code in (
+    (dict(layout=0), INVALID), (dict(d=96), UNSUPPORTED), (dict(workspace=0), INVALID), (dict(workspace=P + 8), INVALID),
+    (dict(size=1), SHAPE))
+] + [(name, bad, code) for name in ("weights", "step", "tree") for bad, code in (
+    (dict(scale=0.0), INVALID), (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID),
+    (dict(heads=0), SHAPE), (dict(kv_heads=0), SHAPE))
+] + [(name, dict(batch=0), SHAPE) for name in ("step", "evict", "tree")]
+
+
+@pytest.mark.parametrize("name,bad,code", BAD)
+def test_refused(lay, name, bad, code):
+    call, args = CALLS[name]
+    assert _status(call, args(lay, **bad)) == code
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_only_the_host_only_layout_is_wrong_with_the_arguments_above(lay, name):
+    """Each list of arguments passes every check but the last: so each change above is what was refused."""
+    call, args = CALLS[name]
+    with pytest.raises(bsa.BsaError, match="host-only"):
+        call(*args(lay).values())
+
+
+def test_an_unsupported_block_size_is_refused():
+    odd = bsa.Layout(OL.BAND_GLOBAL, 100, 32, 1, -1, window=1, global_first=0)
+    for name, (call, args) in CALLS.items():
+        bad = dict(B=32, n=100) if name == "weights" else {}
+        assert _status(call, args(odd, **bad)) == UNSUPPORTED
+    odd.close()
+
+
+def test_workspace_sizes(lay):
+    """0 where the call is refused, else what the stated parts take."""
+    h = lay.handle
+    assert bsa.bsa_attention_weights_workspace_bytes(0, 8, 4) == 0
+    assert bsa.bsa_attention_weights_workspace_bytes(h, 6, 4) == 0
+    col_ptr, _ = bsa.bsa_layout_csc(h)
+    nb = len(col_ptr) // 2
+    slots = max(col_ptr[(x + 1) * nb] // 16 - col_ptr[x * nb] // 16 for x in range(2)) + nb + 1
+    assert bsa.bsa_attention_weights_workspace_bytes(h, 8, 4) == 8 * slots * B * 4
+    # every run of a column has a row of its own among them
+    for x in range(2):
+        seen = set()
+        for j in range(nb):
+            c0, c1 = col_ptr[x * nb + j], col_ptr[x * nb + j + 1]
+            for e in range(c0, c1, 16):
+                slot = e // 16 - col_ptr[x * nb] // 16 + j
+                assert slot not in seen and 0 <= slot < slots
+                seen.add(slot)
+    assert bsa.bsa_evict_workspace_bytes(h, 2, 4, 0) == 0
+    assert bsa.bsa_evict_workspace_bytes(h, 2, 4, 100) >= 4 * 100 * 4 * 2
+    # a budget past the layout's tokens needs no more than one of all of them
+    assert bsa.bsa_evict_workspace_bytes(h, 2, 4, 1 << 30) == bsa.bsa_evict_workspace_bytes(h, 2, 4, N)
+    assert bsa.bsa_decode_weights_workspace_bytes(h, 2, 8, 4, 96) == 0
+    assert bsa.bsa_decode_weights_workspace_bytes(h, 2, 8, 4, 64) > 0
+    assert bsa.bsa_decode_tree_workspace_bytes(h, 2, 8, 4, 129, 64) == 0
+    small, large = (bsa.bsa_decode_tree_workspace_bytes(h, 2, 8, 4, T, 64) for T in (1, 128))
+    assert 0 < small < large
+
+
+def test_sizes_that_pass_32_bits_are_refused_not_wrapped(lay):
+    assert bsa.bsa_decode_tree_workspace_bytes(lay.handle, 1, 1 << 30, 2, 128, 64) == 0
+    assert bsa.bsa_evict_workspace_bytes(lay.handle, 1, (1 << 31) - 1, 10) == 0
+    assert bsa.bsa_attention_weights_workspace_bytes(lay.handle, (1 << 30), 1 << 30) == 0
+    assert ctypes.sizeof(ctypes.c_size_t) == 8
