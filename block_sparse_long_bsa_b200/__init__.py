@@ -19,6 +19,7 @@ Names follow the C ABI: ``bsa_build_layout``, ``bsa_layout_csr``,
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -66,6 +67,8 @@ _lib_lock = threading.Lock()
 def load_library(path: str = LIB_PATH):
     """Load (once) and return the ctypes handle; raises if the library is absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lib_lock:
         if _lib is not None:
             return _lib
@@ -160,6 +163,9 @@ def _stream(s) -> int:
     if s is None:
         try:
             import torch
+            if torch.cuda.is_initialized():
+                # the handle alone: building a Stream object takes several times as long
+                return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
             if torch.cuda.is_available():
                 return torch.cuda.current_stream().cuda_stream
         except ImportError:
@@ -383,7 +389,7 @@ def bsa_attention_weights(q, k, lse, layout: int, B: int, n: int, heads: int, kv
     """Enqueue the sum of the weights that a prompt's keys receive (see include/bsa.h)."""
     lib = load_library()
     _check(lib.bsa_attention_weights(_ptr(q), _ptr(k), _ptr(lse), layout, B, n, heads, kv_heads, d,
-                                     ctypes.c_float(scale), _ptr(weights), weights_stride, _ptr(workspace),
+                                     scale, _ptr(weights), weights_stride, _ptr(workspace),
                                      workspace_bytes, _stream(stream)))
 
 
@@ -397,7 +403,7 @@ def bsa_decode_weights(q, k_cache, v_cache, page_table, max_blocks: int, num_pag
     """Enqueue one decode step that adds its weights up (see include/bsa.h)."""
     lib = load_library()
     _check(lib.bsa_decode_weights(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), max_blocks, num_pages,
-                                  _ptr(positions), layout, batch, heads, kv_heads, d, ctypes.c_float(scale), _ptr(o),
+                                  _ptr(positions), layout, batch, heads, kv_heads, d, scale, _ptr(o),
                                   _ptr(lse), _ptr(weights), weights_stride, _ptr(workspace), workspace_bytes,
                                   _stream(stream)))
 
@@ -428,43 +434,41 @@ def bsa_decode_tree(q, k_tree, v_tree, k_cache, v_cache, page_table, max_blocks:
     lib = load_library()
     _check(lib.bsa_decode_tree(_ptr(q), _ptr(k_tree), _ptr(v_tree), _ptr(k_cache), _ptr(v_cache), _ptr(page_table),
                                max_blocks, num_pages, _ptr(lengths), _ptr(parents), layout, T, batch, heads, kv_heads,
-                               d, ctypes.c_float(scale), _ptr(o), _ptr(lse), _ptr(workspace), workspace_bytes,
+                               d, scale, _ptr(o), _ptr(lse), _ptr(workspace), workspace_bytes,
                                _stream(stream)))
 
 
-def _want(layout: "Layout", **tensors) -> None:
-    """Each tensor (None is skipped) on the layout's device, of its dtype and
-    shape, contiguous; ``name=(tensor, dtype, shape)``, None in a shape for any
-    size."""
-    for name, (t, dtype, shape) in tensors.items():
-        if t is None:
+def _want(device: int, dtype, checks) -> None:
+    """Each (name, tensor, shape) contiguous, of the dtype and shape, on the
+    device; None is skipped."""
+    for name, t, shape in checks:
+        if t is None or (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device):
             continue
-        if t.dtype != dtype or not t.is_contiguous():
-            raise BsaError(1, f"{name} must be a contiguous {str(dtype).replace('torch.', '')} tensor")
-        if t.device.type != "cuda" or t.device.index != layout.device:
-            raise BsaError(1, f"{name} is not on the layout's device (cuda:{layout.device})")
-        if len(t.shape) != len(shape) or any(w is not None and w != x for w, x in zip(shape, t.shape)):
-            want = ", ".join("any" if w is None else str(w) for w in shape)
-            raise BsaError(2, f"{name} has shape {tuple(t.shape)}, not ({want})")
+        what = str(dtype).replace("torch.", "")
+        if t.dtype is not dtype or not t.is_contiguous():
+            raise BsaError(1, f"{name} must be a contiguous {what} tensor")
+        if t.get_device() != device:
+            raise BsaError(1, f"{name} is not on the layout's device (cuda:{device})")
+        raise BsaError(2, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
 
 
-def _rows_of(layout: "Layout", rows: int, **tensors) -> int:
+def _rows_of(layout: "Layout", rows: int, checks) -> int:
     """The common distance between the rows of arrays [rows, >= n] whose last
-    dimension is contiguous (None is skipped); ``name=(tensor, dtype)``."""
-    stride = None
-    for name, (t, dtype) in tensors.items():
+    dimension is contiguous; ``checks`` of (name, tensor, dtype), None skipped."""
+    n, stride = layout.n, None
+    for name, t, dtype in checks:
         if t is None:
             continue
-        if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or t.shape[1] < layout.n or t.stride(1) != 1:
+        if t.dtype is not dtype or t.dim() != 2 or t.shape[0] != rows or t.shape[1] < n or t.stride(1) != 1:
             raise BsaError(2, f"{name} must be a {str(dtype).replace('torch.', '')} tensor of {rows} rows of at least "
-                              f"{layout.n}, contiguous along them")
-        if t.device.type != "cuda" or t.device.index != layout.device:
+                              f"{n}, contiguous along them")
+        if t.get_device() != layout.device:
             raise BsaError(1, f"{name} is not on the layout's device (cuda:{layout.device})")
-        here = t.stride(0) if rows > 1 else layout.n
+        here = t.stride(0) if rows > 1 else n
         if stride is not None and here != stride:
             raise BsaError(2, f"{name}: the arrays' rows must be equally far apart")
         stride = here
-    if stride < layout.n:
+    if stride < n:
         raise BsaError(2, "rows overlap")
     return stride
 
@@ -473,7 +477,6 @@ def _on(stream):
     """Context in which torch allocates for ``stream`` (the current one if
     None), so that memory made here is not handed on while the work on the
     stream still uses it."""
-    import contextlib
     import torch
     if stream is None:
         return contextlib.nullcontext()
@@ -482,12 +485,14 @@ def _on(stream):
     return torch.cuda.stream(stream)
 
 
-def _workspace(layout: "Layout", need: int, workspace):
-    """The given workspace, or a new one of ``need`` bytes; (tensor, bytes)."""
+def _workspace(layout: "Layout", need, workspace, stream):
+    """The given workspace, or a new one of ``need()`` bytes that torch holds
+    for ``stream``; (tensor, bytes)."""
     import torch
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=f"cuda:{layout.device}")
-    elif not workspace.is_contiguous() or workspace.device.type != "cuda" or workspace.device.index != layout.device:
+        with _on(stream):
+            workspace = torch.empty(max(need(), 16), dtype=torch.uint8, device=f"cuda:{layout.device}")
+    elif not workspace.is_contiguous() or workspace.get_device() != layout.device:
         raise BsaError(1, f"workspace must be a contiguous tensor on cuda:{layout.device}")
     return workspace, workspace.numel() * workspace.element_size()
 
@@ -500,18 +505,18 @@ def attention_weights(q, k, lse, layout: "Layout", weights=None, scale: float | 
     import torch
     heads, n, d = q.shape
     kv_heads = k.shape[0]
+    dev, h = layout.device, layout.handle
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    with _on(stream):
-        if weights is None:
+    _want(dev, torch.bfloat16, (("q", q, (heads, layout.n, d)), ("k", k, (kv_heads, layout.n, d))))
+    _want(dev, torch.float32, (("lse", lse, (heads, layout.n)),))
+    if weights is None:
+        with _on(stream):
             weights = torch.zeros((kv_heads, n), dtype=torch.float32, device=q.device)
-        need = bsa_attention_weights_workspace_bytes(layout.handle, heads, kv_heads)
-        workspace, size = _workspace(layout, need, workspace)
-    _want(layout, q=(q, torch.bfloat16, (heads, layout.n, d)), k=(k, torch.bfloat16, (kv_heads, layout.n, d)),
-          lse=(lse, torch.float32, (heads, layout.n)))
-    stride = _rows_of(layout, kv_heads, weights=(weights, torch.float32))
-    bsa_attention_weights(q, k, lse, layout.handle, layout.B, n, heads, kv_heads, d, scale, weights, stride,
-                          workspace, size, stream)
+    stride = _rows_of(layout, kv_heads, (("weights", weights, torch.float32),))
+    workspace, size = _workspace(layout, lambda: bsa_attention_weights_workspace_bytes(h, heads, kv_heads), workspace,
+                                 stream)
+    bsa_attention_weights(q, k, lse, h, layout.B, n, heads, kv_heads, d, scale, weights, stride, workspace, size, stream)
     return weights
 
 
@@ -521,24 +526,25 @@ def decode_weights(q, k_cache, v_cache, page_table, positions, layout: "Layout",
     ``weights`` [batch * H_kv, >= n] fp32; returns (o, lse)."""
     import torch
     heads, d = q.shape
-    hkv = k_cache.shape[1]
+    pages, hkv = k_cache.shape[0], k_cache.shape[1]
+    max_blocks = page_table.shape[-1]
+    dev, h = layout.device, layout.handle
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    pages = k_cache.shape[0]
-    with _on(stream):
-        if o is None:
-            o = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty((heads,), dtype=torch.float32, device=q.device)
-        need = bsa_decode_weights_workspace_bytes(layout.handle, batch, heads, batch * hkv, d)
-        workspace, size = _workspace(layout, need, workspace)
-    _want(layout, q=(q, torch.bfloat16, (heads, d)), k_cache=(k_cache, torch.bfloat16, (pages, hkv, layout.B, d)),
-          v_cache=(v_cache, torch.bfloat16, (pages, hkv, layout.B, d)), o=(o, torch.bfloat16, (heads, d)),
-          lse=(lse, torch.float32, (heads,)), page_table=(page_table, torch.int32, (batch, None)),
-          positions=(positions, torch.int32, (batch,)))
-    stride = _rows_of(layout, batch * hkv, weights=(weights, torch.float32))
-    bsa_decode_weights(q, k_cache, v_cache, page_table, page_table.shape[1], pages, positions, layout.handle, batch,
-                       heads, batch * hkv, d, scale, o, lse, weights, stride, workspace, size, stream)
+    if o is None or lse is None:
+        with _on(stream):
+            o = torch.empty_like(q) if o is None else o
+            lse = torch.empty((heads,), dtype=torch.float32, device=q.device) if lse is None else lse
+    cache = (pages, hkv, layout.B, d)
+    _want(dev, torch.bfloat16, (("q", q, (heads, d)), ("k_cache", k_cache, cache), ("v_cache", v_cache, cache),
+                                ("o", o, (heads, d))))
+    _want(dev, torch.int32, (("page_table", page_table, (batch, max_blocks)), ("positions", positions, (batch,))))
+    _want(dev, torch.float32, (("lse", lse, (heads,)),))
+    stride = _rows_of(layout, batch * hkv, (("weights", weights, torch.float32),))
+    workspace, size = _workspace(
+        layout, lambda: bsa_decode_weights_workspace_bytes(h, batch, heads, batch * hkv, d), workspace, stream)
+    bsa_decode_weights(q, k_cache, v_cache, page_table, max_blocks, pages, positions, h, batch, heads, batch * hkv, d,
+                       scale, o, lse, weights, stride, workspace, size, stream)
     return o, lse
 
 
@@ -551,29 +557,27 @@ def evict(k_cache, v_cache, page_table, lengths, weights, layout: "Layout", budg
     import torch
     batch = lengths.shape[0]
     pages, hkv, _, d = k_cache.shape
-    rows = batch * hkv
+    rows, max_blocks = batch * hkv, page_table.shape[-1]
+    dev, h = layout.device, layout.handle
+    if weights_out is None or tokens_out is None or lengths_out is None:
+        def like(dtype):
+            # an output that is not given has its rows as far apart as the weights'
+            return torch.empty_strided(weights.shape, weights.stride(), dtype=dtype, device=weights.device)
 
-    def like(dtype):
-        # an output that is not given has its rows as far apart as the weights'
-        return torch.empty_strided(weights.shape, weights.stride(), dtype=dtype, device=weights.device)
-
-    with _on(stream):
-        if weights_out is None:
-            weights_out = like(torch.float32)
-        if tokens_out is None:
-            tokens_out = like(torch.int32)
-        if lengths_out is None:
-            lengths_out = torch.empty_like(lengths)
-        need = bsa_evict_workspace_bytes(layout.handle, batch, rows, budget)
-        workspace, size = _workspace(layout, need, workspace)
-    _want(layout, k_cache=(k_cache, torch.bfloat16, (pages, hkv, layout.B, d)),
-          v_cache=(v_cache, torch.bfloat16, (pages, hkv, layout.B, d)),
-          page_table=(page_table, torch.int32, (batch, None)), lengths=(lengths, torch.int32, (batch,)),
-          lengths_out=(lengths_out, torch.int32, (batch,)))
-    stride = _rows_of(layout, rows, weights=(weights, torch.float32), tokens=(tokens, torch.int32),
-                      weights_out=(weights_out, torch.float32), tokens_out=(tokens_out, torch.int32))
-    bsa_evict(k_cache, v_cache, page_table, page_table.shape[1], pages, lengths, weights, tokens, layout.handle,
-              batch, rows, d, budget, recent, stride, weights_out, tokens_out, lengths_out, workspace, size, stream)
+        with _on(stream):
+            weights_out = like(torch.float32) if weights_out is None else weights_out
+            tokens_out = like(torch.int32) if tokens_out is None else tokens_out
+            lengths_out = torch.empty_like(lengths) if lengths_out is None else lengths_out
+    cache = (pages, hkv, layout.B, d)
+    _want(dev, torch.bfloat16, (("k_cache", k_cache, cache), ("v_cache", v_cache, cache)))
+    _want(dev, torch.int32, (("page_table", page_table, (batch, max_blocks)), ("lengths", lengths, (batch,)),
+                             ("lengths_out", lengths_out, (batch,))))
+    stride = _rows_of(layout, rows, (("weights", weights, torch.float32), ("tokens", tokens, torch.int32),
+                                     ("weights_out", weights_out, torch.float32),
+                                     ("tokens_out", tokens_out, torch.int32)))
+    workspace, size = _workspace(layout, lambda: bsa_evict_workspace_bytes(h, batch, rows, budget), workspace, stream)
+    bsa_evict(k_cache, v_cache, page_table, max_blocks, pages, lengths, weights, tokens, h, batch, rows, d, budget,
+              recent, stride, weights_out, tokens_out, lengths_out, workspace, size, stream)
     return weights_out, tokens_out, lengths_out
 
 
@@ -585,24 +589,25 @@ def decode_tree(q, k_tree, v_tree, k_cache, v_cache, page_table, lengths, parent
     import torch
     heads, T, d = q.shape
     batch = lengths.shape[0]
-    pages, hkv = k_cache.shape[:2]
+    pages, hkv = k_cache.shape[0], k_cache.shape[1]
+    max_blocks = page_table.shape[-1]
+    dev, h = layout.device, layout.handle
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    with _on(stream):
-        if o is None:
-            o = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty((heads, T), dtype=torch.float32, device=q.device)
-        need = bsa_decode_tree_workspace_bytes(layout.handle, batch, heads, batch * hkv, T, d)
-        workspace, size = _workspace(layout, need, workspace)
-    tree = (batch * hkv, T, d)
-    _want(layout, q=(q, torch.bfloat16, (heads, T, d)), k_tree=(k_tree, torch.bfloat16, tree),
-          v_tree=(v_tree, torch.bfloat16, tree), k_cache=(k_cache, torch.bfloat16, (pages, hkv, layout.B, d)),
-          v_cache=(v_cache, torch.bfloat16, (pages, hkv, layout.B, d)), o=(o, torch.bfloat16, (heads, T, d)),
-          lse=(lse, torch.float32, (heads, T)), page_table=(page_table, torch.int32, (batch, None)),
-          lengths=(lengths, torch.int32, (batch,)), parents=(parents, torch.int32, (batch, T)))
-    bsa_decode_tree(q, k_tree, v_tree, k_cache, v_cache, page_table, page_table.shape[1], pages, lengths, parents,
-                    layout.handle, T, batch, heads, batch * hkv, d, scale, o, lse, workspace, size, stream)
+    if o is None or lse is None:
+        with _on(stream):
+            o = torch.empty_like(q) if o is None else o
+            lse = torch.empty((heads, T), dtype=torch.float32, device=q.device) if lse is None else lse
+    rows, tree, cache = (heads, T, d), (batch * hkv, T, d), (pages, hkv, layout.B, d)
+    _want(dev, torch.bfloat16, (("q", q, rows), ("k_tree", k_tree, tree), ("v_tree", v_tree, tree),
+                                ("k_cache", k_cache, cache), ("v_cache", v_cache, cache), ("o", o, rows)))
+    _want(dev, torch.int32, (("page_table", page_table, (batch, max_blocks)), ("lengths", lengths, (batch,)),
+                             ("parents", parents, (batch, T))))
+    _want(dev, torch.float32, (("lse", lse, (heads, T)),))
+    workspace, size = _workspace(
+        layout, lambda: bsa_decode_tree_workspace_bytes(h, batch, heads, batch * hkv, T, d), workspace, stream)
+    bsa_decode_tree(q, k_tree, v_tree, k_cache, v_cache, page_table, max_blocks, pages, lengths, parents, h, T, batch,
+                    heads, batch * hkv, d, scale, o, lse, workspace, size, stream)
     return o, lse
 
 

@@ -9,11 +9,12 @@
 // independent of the others, and as few as possible are made (attention does
 // not ask for the order of its keys; `tokens` says which token a slot holds).
 //
-// Kernel 1 (select_kernel), a block per (sequence, key/value head): weights
-// become 32-bit keys whose unsigned order is theirs (protected tokens above
-// all), held in shared memory; the budget-th largest is found digit by digit
-// (11, 11 and 10 bits, a histogram each); ties at it go to the lowest slots;
-// ranks of holes and movers come from ballots and a scan over the warps.
+// Kernel 1 (select_kernel), a cluster of blocks per (sequence, key/value
+// head): weights become 32-bit keys whose unsigned order is theirs (protected
+// tokens above all), held in shared memory; the budget-th largest is found
+// digit by digit (11, 11 and 10 bits, a histogram each, summed over the
+// cluster); ties at it go to the lowest slots; ranks of holes and movers come
+// from ballots and scans over warps and blocks.
 // Kernel 2 (move_kernel), a warp per 32 slots: new weights, tokens and
 // lengths, and the moved rows, 16 bytes a lane.  Its bound is memory: 4 d
 // bytes read and written a moved token.
@@ -30,9 +31,12 @@
 namespace bsa {
 namespace evict {
 
-constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048;
-constexpr int kKeysInSmem = 48 * 1024;          // longer rows recompute their keys in every pass
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
+constexpr int kBins = 4 * kSelThreads;          // of an 11-bit digit, four a thread
+static_assert(kBins == 2048, "11-bit digits");
+constexpr int kBatch = 8;                       // loads of a thread in flight
+constexpr int kMaxCluster = 8, kSlotsPerBlock = kBatch * kSelThreads;
+constexpr int kKeysInSmem = 48 * 1024;          // a block with more slots recomputes its keys in every pass
 constexpr int kMoveThreads = 256;
 
 struct Params {
@@ -45,8 +49,8 @@ struct Params {
   float* weights_out;
   int32_t* tokens_out;
   int32_t* lengths_out;
-  int32_t* src;               // [rows][cap]: the slot that slot s takes its token from
-  int32_t* movers;            // [rows][cap]
+  int32_t* src;               // [rows][cap]: s for a kept slot s, -1 - i for the i-th hole
+  int32_t* movers;            // [rows][cap]: the kept slots behind the budget
   int4* meta;                 // [rows]: kept, newest token, 1 if refused, 1 if nothing moves
   uint32_t* status;
   size_t stride;              // of weights, tokens and their outputs
@@ -63,13 +67,49 @@ __device__ __forceinline__ uint32_t key_of(float w) {
   return b >> 31 ? ~b : b | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const Params p) {
+__device__ __forceinline__ int cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return int(r);
+}
+// All threads of all blocks of the cluster; shared memory written before it is
+// seen by the others after it.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(const void* p, int rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(a)
+               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ int ld_peer(uint32_t a) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ int4 ld_peer4(uint32_t a) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
+// A cluster of C blocks per row; block r owns the slots [r per, (r + 1) per).
+// What the blocks have to know of each other (the newest token, a digit's
+// histogram, the holes and movers before a block) each reads from the others'
+// shared memory after a barrier, and nothing read so is written again.
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int C) {
   extern __shared__ uint32_t s_keys[];
-  __shared__ int hist[kBins];
-  __shared__ int s_red[kSelWarps], s_red2[kSelWarps];
-  __shared__ int s_bad, s_newest, s_digit, s_left;
+  __shared__ __align__(16) int hist[3][kBins];
+  __shared__ int s_scan[3][kSelWarps];
+  __shared__ int s_bad, s_newest, s_digit, s_left, s_holes, s_movers;
   grid_release();
-  const int row = blockIdx.x;
+  const int row = blockIdx.x / C, rank = cluster_rank();
   const int b = row / p.hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int len = p.lengths[b];
@@ -81,6 +121,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const Params p) 
   }
   __syncthreads();
   if (!s_bad && len > p.budget) {
+    // every block of the cluster looks at all pages, so all agree
     bool bad = false;
     for (int j = tid; j < (len + p.B - 1) / p.B; j += kSelThreads) {
       const int pg = p.page_table[size_t(b) * p.max_blocks + j];
@@ -88,101 +129,143 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const Params p) 
     }
     if (bad) s_bad = 1;
   }
+#pragma unroll
+  for (int d = 0; d < 3; ++d)
+    for (int x = tid; x < kBins; x += kSelThreads) hist[d][x] = 0;
   __syncthreads();
   if (s_bad) {
-    if (tid == 0) {
+    if (tid == 0 && rank == 0) {
       p.meta[row] = make_int4(0, 0, 1, 1);
       atomicOr(p.status, kStatusBadIndex);
     }
     return;
   }
+  const int per = (len + C * 32 - 1) / (C * 32) * 32;
+  const int first = min(len, rank * per), end = min(len, first + per);
   // the newest token, from which the protected ones are counted back
   int newest = len - 1;
   if (tok) {
     int m = INT32_MIN;
-    for (int s = tid; s < len; s += kSelThreads) m = max(m, tok[s]);
+    for (int s0 = first + tid; s0 < end; s0 += kBatch * kSelThreads) {
+      int t[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) t[i] = s0 + i * kSelThreads < end ? tok[s0 + i * kSelThreads] : INT32_MIN;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) m = max(m, t[i]);
+    }
     m = __reduce_max_sync(0xffffffffu, m);
     if (lane == 0) atomicMax(&s_newest, m);
-    __syncthreads();
-    newest = len > 0 ? s_newest : -1;
+    cluster_sync();
+    newest = INT32_MIN;
+    for (int r = 0; r < C; ++r) newest = max(newest, ld_peer(peer_addr(&s_newest, r)));
+    if (len == 0) newest = -1;
   }
   if (len <= p.budget) {
-    if (tid == 0) p.meta[row] = make_int4(len, newest, 0, 1);
+    if (tid == 0 && rank == 0) p.meta[row] = make_int4(len, newest, 0, 1);
+    cluster_sync();                      // the others may still be reading s_newest here
     return;
   }
   const int64_t floor_tok = int64_t(newest) - p.recent;      // tokens above it are protected
-  auto make_key = [&](int s) -> uint32_t {
-    const int t = tok ? tok[s] : s;
-    return int64_t(t) > floor_tok ? 0xffffffffu : key_of(w[s]);
-  };
-  const bool held = len <= kKeysInSmem;
-  if (held)
-    for (int s = tid; s < len; s += kSelThreads) s_keys[s] = make_key(s);
-  auto key_at = [&](int s) -> uint32_t { return held ? s_keys[s] : make_key(s); };
+  auto key_from = [&](int t, float x) -> uint32_t { return int64_t(t) > floor_tok ? 0xffffffffu : key_of(x); };
+  auto make_key = [&](int s) -> uint32_t { return key_from(tok ? tok[s] : s, w[s]); };
+  const bool held = per <= kKeysInSmem;
+  if (held) {
+    for (int s0 = first + tid; s0 < end; s0 += kBatch * kSelThreads) {
+      float x[kBatch];
+      int t[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int s = s0 + i * kSelThreads;
+        x[i] = s < end ? w[s] : 0.f;
+        t[i] = tok && s < end ? tok[s] : s;
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (s0 + i * kSelThreads < end) s_keys[s0 - first + i * kSelThreads] = key_from(t[i], x[i]);
+    }
+  }
+  auto key_at = [&](int s) -> uint32_t { return held ? s_keys[s - first] : make_key(s); };
 
   // ---- the budget-th largest key, from the highest digit down
   uint32_t prefix = 0, mask = 0;
   int left = p.budget;                   // how many of the keys under the prefix are kept
-  const int shifts[3] = {21, 10, 0}, bits[3] = {11, 11, 10};
+  int ties0 = 0;                         // keys equal to the last one, in the blocks before this one
+  constexpr int kShift[3] = {21, 10, 0}, kBits[3] = {11, 11, 10};
 #pragma unroll
   for (int d = 0; d < 3; ++d) {
-    for (int x = tid; x < kBins; x += kSelThreads) hist[x] = 0;
-    __syncthreads();
-    const uint32_t dm = (1u << bits[d]) - 1u;
-    for (int s0 = 0; s0 < len; s0 += kSelThreads) {
-      const int s = s0 + tid;
-      const uint32_t k = s < len ? key_at(s) : 0u;
-      const bool in = s < len && (k & mask) == prefix;
-      const int bin = in ? int(k >> shifts[d] & dm) : -1;
+    const uint32_t dm = (1u << kBits[d]) - 1u;
+    for (int s0 = first; s0 < end; s0 += kSelThreads) {
+      const int s = s0 + tid;            // a thread reads the keys that it wrote
+      const uint32_t k = s < end ? key_at(s) : 0u;
+      const bool in = s < end && (k & mask) == prefix;
+      const int bin = in ? int(k >> kShift[d] & dm) : -1;
       // one bin for the whole warp (a run of equal weights) is one addition
       int same;
       __match_all_sync(0xffffffffu, bin, &same);
       if (same) {
-        if (lane == 0 && bin >= 0) atomicAdd(&hist[bin], 32);
+        if (lane == 0 && bin >= 0) atomicAdd(&hist[d][bin], 32);
       } else if (in) {
-        atomicAdd(&hist[bin], 1);
+        atomicAdd(&hist[d][bin], 1);
       }
     }
-    __syncthreads();
-    // the digit whose keys from above reach `left`: each thread owns two bins,
-    // thread 0 the highest ones
-    const int hi_bin = kBins - 1 - 2 * tid;
-    const int a = hist[hi_bin], c = hist[hi_bin - 1];
-    int sum = a + c;
+    cluster_sync();
+    // the digit whose keys, counted from above, reach `left`: each thread owns
+    // four bins of the cluster's sum, thread 0 the highest ones
+    const int top = kBins - 4 - 4 * tid;
+    int4 c = make_int4(0, 0, 0, 0);
+    for (int r = 0; r < C; ++r) {
+      const int4 x = ld_peer4(peer_addr(&hist[d][top], r));
+      c.x += x.x;
+      c.y += x.y;
+      c.z += x.z;
+      c.w += x.w;
+    }
+    const int own = c.x + c.y + c.z + c.w;
+    int sum = own;
 #pragma unroll
     for (int off = 1; off < 32; off *= 2) {
       const int y = __shfl_up_sync(0xffffffffu, sum, off);
       if (lane >= off) sum += y;
     }
-    if (lane == 31) s_red[warp] = sum;
+    if (lane == 31) s_scan[d][warp] = sum;
     __syncthreads();
-    int before = 0;
-    for (int x = 0; x < warp; ++x) before += s_red[x];
-    const int incl = before + sum, excl = incl - a - c;      // keys in higher bins than the thread's
-    if (excl < left && left <= incl) {
-      const bool first = left <= excl + a;
-      s_digit = first ? hi_bin : hi_bin - 1;
-      s_left = first ? left - excl : left - excl - a;
+    for (int x = 0; x < warp; ++x) sum += s_scan[d][x];
+    int above = sum - own;               // keys in higher bins than the thread's
+    if (above < left && left <= sum) {
+      const int bin[4] = {c.w, c.z, c.y, c.x};
+      int digit = top + 3;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (above + bin[x] >= left) break;
+        above += bin[x];
+        --digit;
+      }
+      s_digit = digit;
+      s_left = left - above;
     }
     __syncthreads();
-    prefix |= uint32_t(s_digit) << shifts[d];
-    mask |= dm << shifts[d];
+    const int digit = s_digit;
+    prefix |= uint32_t(digit) << kShift[d];
+    mask |= dm << kShift[d];
     left = s_left;
+    if (d == 2)
+      for (int r = 0; r < rank; ++r) ties0 += ld_peer(peer_addr(&hist[d][digit], r));
     __syncthreads();
   }
   // keys above `prefix` are kept, and of those equal to it the first `left`
 
-  // ---- ranks: each warp owns a run of slots
-  const int per = (len + kSelWarps * 32 - 1) / (kSelWarps * 32) * 32;
-  const int lo = min(len, warp * per), hi = min(len, lo + per);
-  auto scan_warps = [&](int* red, int count, int& total) -> int {   // exclusive prefix over the warps
-    if (lane == 0) red[warp] = count;
+  // ---- ranks: each warp owns a run of the block's slots
+  const int wper = (end - first + kSelWarps * 32 - 1) / (kSelWarps * 32) * 32;
+  const int lo = min(end, first + warp * wper), hi = min(end, lo + wper);
+  // how many of a count come before this warp in the block
+  auto before = [&](int* scan, int count, int& total) -> int {
+    if (lane == 0) scan[warp] = count;
     __syncthreads();
     int pre = 0;
     total = 0;
     for (int x = 0; x < kSelWarps; ++x) {
-      if (x < warp) pre += red[x];
-      total += red[x];
+      if (x < warp) pre += scan[x];
+      total += scan[x];
     }
     return pre;
   };
@@ -191,7 +274,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const Params p) 
     const int s = s0 + lane;
     count += __popc(__ballot_sync(0xffffffffu, s < hi && key_at(s) == prefix));
   }
-  const int ties = scan_warps(s_red, count, total);
+  const int ties = ties0 + before(s_scan[0], count, total);
   // kept slots of a ballot, with the ties seen so far
   auto kept_of = [&](int s0, int& seen) -> unsigned {
     const int s = s0 + lane;
@@ -210,31 +293,31 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const Params p) 
     holes += __popc(~kept & low);
     movers += __popc(kept & ~low);
   }
-  int hole0 = scan_warps(s_red2, holes, total);
-  __syncthreads();
-  int mover0 = scan_warps(s_red, movers, total);
+  int hole0 = before(s_scan[1], holes, total);
+  if (tid == 0) s_holes = total;
+  int mover0 = before(s_scan[2], movers, total);
+  if (tid == 0) s_movers = total;
+  cluster_sync();
+  for (int r = 0; r < rank; ++r) {
+    hole0 += ld_peer(peer_addr(&s_holes, r));
+    mover0 += ld_peer(peer_addr(&s_movers, r));
+  }
   int32_t* const mv = p.movers + size_t(row) * p.cap;
   int32_t* const src = p.src + size_t(row) * p.cap;
   seen = ties;
   for (int s0 = lo; s0 < hi; s0 += 32) {
     const unsigned kept = kept_of(s0, seen);
     const int s = s0 + lane;
-    const bool is = kept >> lane & 1u;
-    const unsigned moves = __ballot_sync(0xffffffffu, is && s >= p.budget);
-    if (is && s >= p.budget) mv[mover0 + __popc(moves & ((1u << lane) - 1u))] = s;
-    mover0 += __popc(moves);
-  }
-  __syncthreads();                       // the movers are in memory for the whole block
-  seen = ties;
-  for (int s0 = lo; s0 < min(hi, p.budget); s0 += 32) {
-    const unsigned kept = kept_of(s0, seen);
-    const int s = s0 + lane;
-    const bool hole = s < hi && s < p.budget && !(kept >> lane & 1u);
-    const unsigned hb = __ballot_sync(0xffffffffu, hole);
-    if (s < hi && s < p.budget) src[s] = hole ? mv[hole0 + __popc(hb & ((1u << lane) - 1u))] : s;
+    const bool is = kept >> lane & 1u, low = s < p.budget && s < hi;
+    const unsigned mb = __ballot_sync(0xffffffffu, is && !low), hb = __ballot_sync(0xffffffffu, low && !is);
+    const unsigned under = (1u << lane) - 1u;
+    if (is && !low) mv[mover0 + __popc(mb & under)] = s;
+    if (low) src[s] = is ? s : -1 - (hole0 + __popc(hb & under));
+    mover0 += __popc(mb);
     hole0 += __popc(hb);
   }
-  if (tid == 0) p.meta[row] = make_int4(p.budget, newest, 0, 0);
+  if (tid == 0 && rank == 0) p.meta[row] = make_int4(p.budget, newest, 0, 0);
+  cluster_sync();                        // no block ends while another may still read its shared memory
 }
 
 template <int HD>
@@ -259,6 +342,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const Params p, int 
     int t = int(int64_t(m.y) + 1 + (s - m.x));               // a slot behind takes the next token to come
     if (s < m.x) {
       if (!m.w) from = p.src[size_t(row) * p.cap + s];
+      if (from < 0) from = p.movers[size_t(row) * p.cap + (-1 - from)];
       wt = p.weights[at + from];
       t = p.tokens ? p.tokens[at + from] : from;
     }
@@ -310,7 +394,8 @@ int check_sizes(const bsa_layout* layout, int batch, int kv_heads, int budget) {
   if (batch < 1 || kv_heads < 1) return set_error(BSA_ERR_SHAPE, "batch and kv_heads must be >= 1");
   if (kv_heads % batch) return set_error(BSA_ERR_SHAPE, "kv_heads must be a multiple of batch");
   if (budget < 1) return set_error(BSA_ERR_SHAPE, "budget must be >= 1");
-  if (int64_t(kv_heads) * ((int64_t(layout->n) + kMoveThreads - 1) / kMoveThreads) > INT32_MAX)
+  if (int64_t(kv_heads) * std::max<int64_t>(kMaxCluster, (int64_t(layout->n) + kMoveThreads - 1) / kMoveThreads) >
+      INT32_MAX)
     return set_error(BSA_ERR_SHAPE, "too many slots");
   return BSA_OK;
 }
@@ -336,9 +421,24 @@ int launch(const Params& p, int rows, int d, cudaStream_t stream) {
       done[dev] = true;
     }
   }
-  const size_t smem = size_t(p.n <= kKeysInSmem ? p.n : kKeysInSmem) * 4;
-  select_kernel<<<unsigned(rows), kSelThreads, smem, stream>>>(p);
-  e = cudaGetLastError();
+  // blocks per row: one for each kSlotsPerBlock slots, so that a thread has one
+  // batch of them
+  int C = 1;
+  while (C < kMaxCluster && p.n > C * kSlotsPerBlock) C *= 2;
+  const int per = (p.n + C * 32 - 1) / (C * 32) * 32;
+  cudaLaunchConfig_t sel = {};
+  sel.gridDim = dim3(unsigned(rows) * unsigned(C), 1, 1);
+  sel.blockDim = dim3(kSelThreads, 1, 1);
+  sel.dynamicSmemBytes = size_t(std::min(per, kKeysInSmem)) * 4;
+  sel.stream = stream;
+  cudaLaunchAttribute cl[1];
+  cl[0].id = cudaLaunchAttributeClusterDimension;
+  cl[0].val.clusterDim.x = unsigned(C);
+  cl[0].val.clusterDim.y = 1;
+  cl[0].val.clusterDim.z = 1;
+  sel.attrs = cl;
+  sel.numAttrs = 1;
+  e = cudaLaunchKernelEx(&sel, select_kernel, p, C);
   if (e != cudaSuccess) return set_error(BSA_ERR_CUDA, std::string("eviction select launch: ") + cudaGetErrorString(e));
   const int tiles = (p.n + kMoveThreads - 1) / kMoveThreads;
   cudaLaunchConfig_t cfg = {};

@@ -87,7 +87,7 @@ Plan plan_of(const bsa_layout* L, int batch, int heads, int kv_heads, int T) {
   const int64_t busy = int64_t(batch) * p.hg * p.mtiles;
   p.units = int(std::min<int64_t>(busy * p.groups, INT32_MAX));
   const int chunks = std::max(1, L->max_row * (L->B / kChunk));
-  const int fill = int(std::min<int64_t>(chunks, std::max<int64_t>(1, (kSlots + busy - 1) / busy)));
+  const int fill = int(std::min<int64_t>(chunks, std::max<int64_t>(1, kSlots / busy)));
   p.S = std::max(fill, (chunks + kRunChunks - 1) / kRunChunks);
   p.cap = std::min(kTileM, p.rows);
   return p;
@@ -127,7 +127,7 @@ struct Params {
   uint32_t* status;
   size_t score_stride;
   int n, nb, L, H, hkv, max_blocks, num_pages, max_row;
-  int hg, hpt, rows, mtiles, groups, S, cap, T, tiles;
+  int hg, hpt, rows, mtiles, per_group, S, cap, T, tiles;   // per_group: units of a layout row
   float scale_log2;
 };
 
@@ -231,11 +231,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     return;
   }
   grid_release();
+  // the later layout rows' units last: most of them have nothing to do
   const int run = blockIdx.x % p.S;
   const int unit = blockIdx.x / p.S;
-  const int grp = unit % p.groups;
-  const int mt = unit / p.groups % p.mtiles;
-  const int bh = unit / p.groups / p.mtiles;      // (sequence, head group)
+  const int grp = unit / p.per_group;
+  const int mt = unit % p.per_group % p.mtiles;
+  const int bh = unit % p.per_group / p.mtiles;   // (sequence, head group)
   const int b = bh / p.hg, hg = bh - b * p.hg;
   const int f0 = b * p.H + hg * p.hpt;            // first query head of the tile
   const int hk = p.L == 1 ? hg : hg / (p.H / p.hkv);
@@ -598,21 +599,31 @@ __device__ __forceinline__ int join_runs(const Params& p, int unit, int row, flo
     }
     const unsigned live = __ballot_sync(0xffffffffu, w != 0.f);
     const int n = min(32, p.S - s0);
-#pragma unroll 4
-    for (int x = 0; x < n; ++x) {
-      const float wx = __shfl_sync(0xffffffffu, w, x);
-      if (!(live >> x & 1u)) continue;
-      const float* src = p.part_o + ((size_t(unit) * p.S + s0 + x) * p.cap + row) * HD + lane * DPL;
-      if constexpr (DPL == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        acc[0] += wx * v.x;
-        acc[1] += wx * v.y;
-        acc[2] += wx * v.z;
-        acc[3] += wx * v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        acc[0] += wx * v.x;
-        acc[1] += wx * v.y;
+    const float* src = p.part_o + ((size_t(unit) * p.S + s0) * p.cap + row) * HD + lane * DPL;
+    const size_t step = size_t(p.cap) * HD;
+    constexpr int U = 8;                 // runs in flight; one that wrote nothing is not read
+    for (int x0 = 0; x0 < n; x0 += U) {
+      float v[U][DPL];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool on = x0 + u < n && (live >> (x0 + u) & 1u);
+        if constexpr (DPL == 4) {
+          const float4 t = on ? *reinterpret_cast<const float4*>(src + (x0 + u) * step) : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[u][0] = t.x;
+          v[u][1] = t.y;
+          v[u][2] = t.z;
+          v[u][3] = t.w;
+        } else {
+          const float2 t = on ? *reinterpret_cast<const float2*>(src + (x0 + u) * step) : make_float2(0.f, 0.f);
+          v[u][0] = t.x;
+          v[u][1] = t.y;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float wx = __shfl_sync(0xffffffffu, w, (x0 + u) & 31);
+#pragma unroll
+        for (int e = 0; e < DPL; ++e) acc[e] = fmaf(x0 + u < n ? wx : 0.f, v[u][e], acc[e]);
       }
     }
   }
@@ -635,7 +646,7 @@ __device__ __forceinline__ void store_row(const Params& p, size_t row, bool refu
   if (lane == 0) p.lse[row] = none ? -INFINITY : (M + __log2f(L)) * kLn2;
 }
 
-// Does row `at` of the layout keep block j?
+// Block j's place in row `at` of the layout, -1 if the row does not keep it.
 __device__ __forceinline__ int find_block(const Params& p, size_t at, int j) {
   int lo = p.row_ptr[at], hi = p.row_ptr[at + 1];
   const int first = lo;
@@ -647,10 +658,14 @@ __device__ __forceinline__ int find_block(const Params& p, size_t at, int j) {
   return lo < p.row_ptr[at + 1] && p.col_idx[lo] == j ? lo - first : -1;
 }
 
-// The step: blocks [0, row_blocks) join one row per warp; the others turn
-// the scores of 256 list keys of a key/value head into weights.
+// The step: blocks [0, row_blocks) join one row per warp; the others turn the
+// scores of kTileKeys list keys of a key/value head into weights, four keys a
+// thread (one block a 256 keys spent its time on finding M and L: 82 us for
+// the 16 x 16K step, against 23 so).
+constexpr int kTileKeys = 4 * kJoinWarps * 32;
+
 template <int BLK, int HD>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_step_kernel(const Params p, int heads, int row_blocks) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 1) join_step_kernel(const Params p, int heads, int row_blocks) {
   __shared__ float s_m[32], s_l[32];
   __shared__ int s_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -671,10 +686,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_step_kernel(const Params
     if (lane == 0 && (!in || (flag & 1))) atomicOr(p.status, kStatusBadIndex);
     return;
   }
-  // ---- weights.  With one route for all heads a block takes 256 list keys of
-  // a key/value head and sums its query heads; with a route per head it takes
-  // 256 list keys of one query head, and of the key blocks that several heads
-  // of the group keep each is summed by the first of them.
+  // ---- weights.  With one route for all heads a block takes list keys of a
+  // key/value head and sums its query heads; with a route per head it takes
+  // list keys of one query head, and of the key blocks that several heads of
+  // the group keep each is summed by the first of them.
   const int x = blockIdx.x - row_blocks;
   const int tile = x % p.tiles, hg = x / p.tiles;           // hg over batch * head groups
   const int g = p.H / p.hkv;
@@ -682,14 +697,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_step_kernel(const Params
   const int t = p.lengths[b];
   if (t < 0 || t >= p.n) return;
   const size_t at0 = size_t((b * p.H + h0) % p.L) * p.nb + t / BLK;
-  const int list = (p.row_ptr[at0 + 1] - p.row_ptr[at0]) * BLK;
-  if (tile * 256 >= list) return;
+  const int start = p.row_ptr[at0], list = (p.row_ptr[at0 + 1] - start) * BLK;
+  if (tile * kTileKeys >= list) return;
   const int kv = h0 / g, first = p.L == 1 ? h0 : kv * g;    // first query head of the group
-  const int k0 = tile * 256 + threadIdx.x;
-  const int j = k0 < list ? p.col_idx[p.row_ptr[at0] + k0 / BLK] : -1;
+  const int k0 = tile * kTileKeys + threadIdx.x * 4;        // four keys of one block
+  const int j = k0 < list ? p.col_idx[start + k0 / BLK] : -1;
   const int u = j * BLK + k0 % BLK;
   bool mine = j >= 0 && u <= t;
-  float sum = 0.f;
+  float* const to = p.weights + size_t(b * p.hkv + kv) * p.weights_stride + u;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f}, old[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) old[e] = mine && u + e <= t ? to[e] : 0.f;
   // up to 32 query heads of the group at a time: their M and L, then their scores
   for (int h1 = 0; h1 < g; h1 += 32) {
     const int count = min(32, g - h1);
@@ -704,22 +722,24 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_step_kernel(const Params
       for (int s = lane; s < p.S; s += 32) {
         flag |= p.part_flag[size_t(unit) * p.S + s];
         const float2 ml = p.part_ml[(size_t(unit) * p.S + s) * p.cap + row];
-        if (ml.y != 0.f) M = fmaxf(M, ml.x);
+        if (ml.y == 0.f) continue;
+        const float m = fmaxf(M, ml.x);
+        // L stays under the running max; -inf only while every l seen is a NaN's
+        L = (M == -INFINITY ? L : L * ex2(M - m)) + (ml.x == -INFINITY ? ml.y : ml.y * ex2(ml.x - m));
+        M = m;
       }
+      const float mine_m = M;
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-      for (int s = lane; s < p.S; s += 32) {
-        const float2 ml = p.part_ml[(size_t(unit) * p.S + s) * p.cap + row];
-        if (ml.y != 0.f) L += (M == -INFINITY ? 1.f : ex2(ml.x - M)) * ml.y;
-      }
+      if (mine_m != -INFINITY) L *= ex2(mine_m - M);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-      if (lane == 0) {
-        s_m[h] = M;
-        s_l[h] = L;
-      }
       flag = __reduce_or_sync(0xffffffffu, flag);
-      if (lane == 0 && flag) atomicOr(&s_flag, 1 << h);
+      if (lane == 0) {
+        s_m[h] = M == -INFINITY ? 0.f : -M;
+        s_l[h] = L;
+        if (flag) atomicOr(&s_flag, 1 << h);
+      }
     }
     __syncthreads();
     if (mine) {
@@ -736,20 +756,28 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_step_kernel(const Params
           k = e * BLK + k0 % BLK;
         }
         // a refused row and a row without any weight add nothing
-        if ((s_flag >> h & 1) || s_l[h] == 0.f) continue;
-        const float s = p.scores[size_t(b * p.H + hh) * p.score_stride + k];
-        const float m = s_m[h];
-        sum += ex2(fmaf(s, p.scale_log2, m == -INFINITY ? 0.f : -m)) / s_l[h];
+        const float l = s_l[h];
+        if ((s_flag >> h & 1) || l == 0.f) continue;
+        const float4 sc = *reinterpret_cast<const float4*>(p.scores + size_t(b * p.H + hh) * p.score_stride + k);
+        const float neg = s_m[h], inv = 1.f / l;
+        sum[0] = fmaf(ex2(fmaf(sc.x, p.scale_log2, neg)), inv, sum[0]);
+        sum[1] = fmaf(ex2(fmaf(sc.y, p.scale_log2, neg)), inv, sum[1]);
+        sum[2] = fmaf(ex2(fmaf(sc.z, p.scale_log2, neg)), inv, sum[2]);
+        sum[3] = fmaf(ex2(fmaf(sc.w, p.scale_log2, neg)), inv, sum[3]);
       }
     }
   }
-  if (mine) p.weights[size_t(b * p.hkv + kv) * p.weights_stride + u] += sum;
+  if (mine) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (u + e <= t) to[e] = old[e] + sum[e];
+  }
 }
 
 // The tree: one row (query head, drafted token) per warp, its runs joined with
 // its ancestors' keys.
 template <int BLK, int HD>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_tree_kernel(const Params p) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 3) join_tree_kernel(const Params p) {
   constexpr int DPL = HD / 32, CPL = HD / 8;
   __shared__ int s_par[kMaxT];
   __shared__ int s_path[kJoinWarps][kMaxT];       // ancestors from the token up to its root
@@ -784,9 +812,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_tree_kernel(const Params
   // the layout row of the token, and which of the blocks that its path lies in it keeps
   const int blk = pos / BLK, blk0 = bad ? 0 : len / BLK;
   const size_t at = size_t(f % p.L) * p.nb + blk;
-  bool kept = false;
-  if (live && !bad && lane <= blk - blk0) kept = find_block(p, at, blk0 + lane) >= 0;
-  const unsigned keeps = __ballot_sync(0xffffffffu, kept);
+  // (they are the row's last entries: its columns ascend up to the row itself)
+  unsigned keeps = 0;
+  if (live && !bad && lane <= blk - blk0) {
+    const int e = p.row_ptr[at + 1] - 1 - lane;
+    const int j = e >= p.row_ptr[at] ? p.col_idx[e] : -1;
+    if (j >= blk0) keeps = 1u << (j - blk0);
+  }
+  keeps = __reduce_or_sync(0xffffffffu, keeps);
   const int grp = blk - blk0;
   // scores of the ancestors: 8 lanes a key, four keys at a time
   const int sub = lane >> 3, pc = lane & 7;
@@ -839,7 +872,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_tree_kernel(const Params
   int flag = 0;
   if (!bad) {
     const int row = hh % p.hpt * p.T + i;
-    const int unit = ((b * p.hg + hh / p.hpt) * p.mtiles + row / kTileM) * p.groups + grp;
+    const int unit = grp * p.per_group + (b * p.hg + hh / p.hpt) * p.mtiles + row / kTileM;
     flag = join_runs<HD>(p, unit, row % kTileM, M, L, acc);
     // the cache's part and the path's under one max
     const float all = fmaxf(M, top);
@@ -1031,11 +1064,11 @@ int run(bool tree, const void* q, const void* k_tree, const void* v_tree, const 
   p.hpt = pl.hpt;
   p.rows = pl.rows;
   p.mtiles = pl.mtiles;
-  p.groups = pl.groups;
+  p.per_group = pl.units / pl.groups;
   p.S = pl.S;
   p.cap = pl.cap;
   p.T = T;
-  p.tiles = std::max(1, (layout->max_row * layout->B + 255) / 256);
+  p.tiles = std::max(1, (layout->max_row * layout->B + kTileKeys - 1) / kTileKeys);
   p.scale_log2 = float(double(scale) * 1.4426950408889634);
   const Call c{q, k_cache, v_cache, batch, heads, kv_heads, pl, static_cast<cudaStream_t>(stream)};
   const int B = layout->B;

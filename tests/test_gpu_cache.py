@@ -301,7 +301,8 @@ EVICT = [
     (2500, 128, 1, 2, 64, 2400, 300, [2500], True),
     (5000, 64, 2, 1, 128, 64, 32, [4999, 65], False),
     (64, 64, 1, 1, 64, 100, 3, [64], False),                # a budget past the cache: nothing to cut
-    (70000, 128, 1, 1, 64, 30001, 500, [69999], True),      # longer than the keys that shared memory holds
+    (70000, 128, 1, 1, 64, 30001, 500, [69999], True),      # a cluster of blocks for each row
+    (400000, 128, 1, 1, 64, 100001, 500, [399999], True),   # longer than the keys that their shared memory holds
 ]
 
 
