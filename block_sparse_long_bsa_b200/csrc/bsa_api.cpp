@@ -100,7 +100,8 @@ int bsa_build_layout(const bsa_pattern* spec, int n, int B, int layout_heads, in
     const size_t o_sp = o_ri + round_up(b_ri, 256), o_sg = o_sp + round_up(b_sp, 256);
     const size_t b_wk = lay->work.size() * sizeof(int32_t);
     const size_t o_wk = o_sg + round_up(b_sg, 256);
-    const size_t o_st = o_wk + round_up(b_wk, 256), total = o_st + bsa::kStatusBlockBytes;
+    const size_t o_ps = o_wk + round_up(b_wk, 256);
+    const size_t o_st = o_ps + round_up(b_ri, 256), total = o_st + bsa::kStatusBlockBytes;
     void* base = nullptr;
     e = cudaMalloc(&base, total);
     if (e != cudaSuccess) {
@@ -120,6 +121,8 @@ int bsa_build_layout(const bsa_pattern* spec, int n, int B, int layout_heads, in
     if (e == cudaSuccess && !lay->row_idx.empty())
       e = cudaMemcpy(c + o_ri, lay->row_idx.data(), lay->row_idx.size() * sizeof(int32_t),
                      cudaMemcpyHostToDevice);
+    if (e == cudaSuccess && !lay->csr_pos.empty())
+      e = cudaMemcpy(c + o_ps, lay->csr_pos.data(), lay->csr_pos.size() * sizeof(int32_t), cudaMemcpyHostToDevice);
     if (e == cudaSuccess) e = cudaMemcpy(c + o_sp, lay->seg_ptr.data(), b_sp, cudaMemcpyHostToDevice);
     if (e == cudaSuccess && !lay->segs.empty())
       e = cudaMemcpy(c + o_sg, lay->segs.data(), lay->segs.size() * sizeof(int32_t), cudaMemcpyHostToDevice);
@@ -137,6 +140,7 @@ int bsa_build_layout(const bsa_pattern* spec, int n, int B, int layout_heads, in
     lay->d_order = reinterpret_cast<const int32_t*>(c + o_or);
     lay->d_col_ptr = reinterpret_cast<const int32_t*>(c + o_cp);
     lay->d_row_idx = reinterpret_cast<const int32_t*>(c + o_ri);
+    lay->d_csr_pos = reinterpret_cast<const int32_t*>(c + o_ps);
     lay->d_seg_ptr = reinterpret_cast<const int32_t*>(c + o_sp);
     lay->d_segs = reinterpret_cast<const int32_t*>(c + o_sg);
     lay->d_work = reinterpret_cast<const int32_t*>(c + o_wk);

@@ -5,23 +5,28 @@
 // the column sums of the forward's probabilities, rebuilt from its lse as the
 // gradients rebuild them; no n x n matrix exists.
 //
-// One work item is a run of at most 16 query blocks of a key block's column of
-// the transposed layout (the segments of the key/value gradients) against one
-// 64-key chunk of that block.  The chunk's keys stay in shared memory for the
-// whole run; the query rows that read them stream past in 128-row tiles (two
-// blocks of 64, or one of 128):
-//   S = Q K^T                 (tcgen05.mma, bf16 x bf16 -> fp32 in TMEM)
-//   acc[c] += exp2(S[r][c] scale log2 e - lse_r log2 e)
-// A thread owns one tile row and keeps the 64 running sums of its row slot in
-// registers, so the sum over rows is taken once per run, not per tile: a
-// transposing butterfly inside each warp, then the four warps in order.  All
-// sums are fp32 and their order is fixed by the layout alone, so results do
-// not change from run to run: runs leave partial sums in the caller's
-// workspace and a second kernel adds each column's runs in order.
+// One work item is a query block row (for B = 64 of two query heads that share
+// a key/value head and a route, else of one): its NQ <= 128 query rows stay in
+// shared memory while the row's kept key blocks stream past, 128 keys at a
+// time.  The product is taken with the keys as its rows,
+//   S^T = K Q^T               (tcgen05.mma, bf16 x bf16 -> fp32 in TMEM)
+// so that a TMEM lane is a key and the sum over queries, of
+// exp2(S^T[u][t] scale log2 e - lse_t log2 e), stays inside a thread: no value
+// crosses lanes, and a tile costs its exponentials, one fused multiply-add and
+// one addition each.  The exponentials are the bound: 16 a clock and SM.
 //
-// Roles (192 threads, two CTAs per SM): warp 0 issues the TMA loads, warp 1
-// the products, warps 2-5 hold the rows.  Every wait is bounded as in the
-// forward.
+// Each kept block leaves its B sums in the caller's workspace, and a second
+// kernel adds each key's sums up in row order, so all sums are fp32 in an
+// order that the layout alone fixes.  Key/value heads whose kept blocks need
+// more than kStripBytes together are worked off in turns that share the workspace.
+//
+// Roles (448 threads, one CTA per SM): warp 0 looks items up and issues the TMA
+// loads, warp 1 the products; warps 2-13 take the sums in three groups, each a
+// tile of its own with a thread per key, so that on every scheduler one group
+// waits, loads and stores while the others' exponentials run.  (Sixteen warps
+// on one tile, four threads a key, met at a barrier per tile and left the
+// exponential unit idle in between: 175 us for the 32K dyadic route.)  Every
+// wait is bounded as in the forward.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -41,84 +46,77 @@ namespace wts {
 
 using namespace ptx;
 
-constexpr int kThreads = 192;
-constexpr int kTileM = 128;
-constexpr int kChunk = 64;           // keys of a work item
-constexpr int kQSlots = 2, kKSlots = 2, kSBufs = 4;
+constexpr int kGroups = 3;           // groups of four key warps, a tile each
+constexpr int kThreads = 64 + 128 * kGroups;
+constexpr int kTileM = 128;          // keys of a tile
+constexpr int kQSlots = 2, kKSlots = 4;
+constexpr int kSBufs = 4;            // S buffers, one more than groups: the next product is ready in time
+// A group that is still at tile t lets the products get to t + 3, and the
+// producer is two items ahead of them: at most seven items are in use at once.
+constexpr int kItems = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint64_t kWaitNs = 1000000000ull, kDrainNs = 200000000ull;
+constexpr size_t kStripBytes = size_t(64) << 20;
 
 struct Params {
+  const int32_t* row_ptr;
+  const int32_t* col_idx;
   const int32_t* col_ptr;
-  const int32_t* row_idx;
-  const int32_t* seg_ptr;
-  const int32_t* segs;
+  const int32_t* csr_pos;
   const float* lse;
-  float* part;               // [head group][slot][B]
+  float* part;               // [unit][slots][B]
   float* weights;
   size_t weights_stride;
   uint32_t* status;
-  int n, nb, L, g, kv_heads;
-  int hpg;                   // query heads of a head group: a key/value head's, or one when routes differ by head
-  int groups;                // head groups
-  int max_segs, slots;
-  int64_t items;             // groups * max_segs * chunks of a block
+  int n, nb, L, g, heads;
+  int pack;                  // query heads of a unit
+  int upk;                   // units of a key/value head
+  int kv0, kvs;              // the strip's key/value heads
+  int64_t slots;             // kept blocks that a unit has room for
+  uint32_t items;            // units of the strip * nb
   float scale_log2;
 };
 
-template <int BLK, int HD>
+template <int BLK, int HD, int PACK>
 struct Shape {
-  static constexpr int kCPB = BLK / kChunk;
-  static constexpr int kSubs = kTileM / BLK;                  // query blocks of a tile
-  static constexpr int kQBytes = kTileM * HD * 2;
-  static constexpr int kKBytes = kChunk * HD * 2;
-  static constexpr int kAtomQ = kTileM * 128, kAtomK = kChunk * 128;
+  static constexpr int kNQ = BLK * PACK;                      // query rows of an item
+  static constexpr int kBPT = kTileM / BLK;                   // key blocks of a tile
+  static constexpr int kQBytes = kNQ * HD * 2;
+  static constexpr int kKBytes = kTileM * HD * 2;
+  static constexpr int kAtomQ = kNQ * 128, kAtomK = kTileM * 128;
   static constexpr int kOffK = kQSlots * kQBytes;
-  static constexpr int kOffRed = kOffK + kKSlots * kKBytes;   // [2][4 warps][64] partial column sums
-  static constexpr int kOffBar = kOffRed + 2 * 4 * kChunk * 4;
-  // q_full, q_free, k_full, k_free, s_full, s_free, drain
-  static constexpr int kNumBars = 2 * kQSlots + 2 * kKSlots + 2 * kSBufs + 1;
+  static constexpr int kOffNeg = kOffK + kKSlots * kKBytes;   // [kItems][128] -lse log2 e
+  static constexpr int kOffItem = kOffNeg + kItems * 128 * 4;
+  static constexpr int kOffBar = kOffItem + kItems * 32;
+  // q_full, q_free, k_full, k_free, s_full, s_free, item, drain
+  static constexpr int kNumBars = 2 * kQSlots + 2 * kKSlots + 2 * kSBufs + kItems + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kSmem = kOffMisc + 16;
-  static constexpr uint32_t kTmemCols = kSBufs * kChunk;      // 256
-  static constexpr uint32_t kIdesc = idesc_bf16(kTileM, kChunk, 0, 0);
+  static constexpr int kUsed = kOffMisc + 16;
+  // more than half of an SM's shared memory, so that no second CTA shares it:
+  // an item's S buffers take up to all of TMEM
+  static constexpr int kSmem = kUsed < 116 * 1024 ? 116 * 1024 : kUsed;
+  static constexpr uint32_t kTmemCols = kSBufs * kNQ;         // 256 or 512
+  static constexpr uint32_t kIdesc = idesc_bf16(kTileM, kNQ, 0, 0);
+  static_assert(kNQ == 64 || kNQ == 128, "query rows of an item");
+  static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
-// A work item, decoded the same way by every role.
+// A work item as the producer announces it; tiles 0 ends the stream.
 struct Item {
-  int j, e0, units;          // key block, first entry of the run, (query block, head) pairs
-  int kv, f0, chunk;         // key/value head, first query head, 64-key chunk of the block
-  size_t slot;               // row of the partial sums
+  int tiles, blocks;         // tiles and kept blocks of the row
+  int diag;                  // the last kept block is the diagonal one
+  int dead;                  // a query row of the item has lse = -inf
+  int64_t slot;              // first row of partial sums
+  int64_t pad;
 };
+static_assert(sizeof(Item) == 32, "item ring");
 
-template <int BLK>
-__device__ __forceinline__ bool decode(const Params& p, int64_t it, Item& x) {
-  constexpr int CPB = BLK / kChunk;
-  const int per = p.max_segs * CPB;
-  const int grp = int(it / per), rest = int(it - int64_t(grp) * per);
-  const int seg = rest / CPB;
-  x.chunk = rest - seg * CPB;
-  x.f0 = grp * p.hpg;
-  x.kv = x.f0 / p.g;
-  const int lh = x.f0 % p.L;
-  const int s0 = p.seg_ptr[lh];
-  if (seg >= p.seg_ptr[lh + 1] - s0) return false;
-  const int32_t* s = p.segs + 3 * size_t(s0 + seg);
-  x.j = s[0];
-  x.e0 = s[1];
-  x.units = s[2] * p.hpg;
-  // entry / 16 + block grows by at least one from run to run (a column's runs
-  // start 16 entries apart, a new column adds its block), so it names the run
-  x.slot = size_t(grp) * p.slots + (x.e0 / kColumnSegment - p.col_ptr[size_t(lh) * p.nb] / kColumnSegment) + x.j;
-  return true;
-}
-
-__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c) {
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c0, float c1) {
   asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
-      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\tmov.b64 rc, {%5, %5};\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\tmov.b64 rc, {%5, %6};\n\t"
       "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
       : "=f"(d0), "=f"(d1)
-      : "f"(a0), "f"(a1), "f"(b), "f"(c));
+      : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
 }
 __device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
   asm("{\n\t.reg .b64 ra, rd;\n\t"
@@ -127,13 +125,24 @@ __device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
       : "+f"(d0), "+f"(d1)
       : "f"(a0), "f"(a1));
 }
+// Waits for the loads of TMEM into v; the registers are operands so that no
+// use of them is moved before it while other loads are in flight.
+__device__ __forceinline__ void wait_ld32(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]),
+                 "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
+                 "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
+}
 
-template <int BLK, int HD>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int BLK, int HD, int PACK>
+__global__ void __launch_bounds__(kThreads, 1)
     prompt_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                           const Params p) {
-  using S = Shape<BLK, HD>;
-  constexpr int SUBS = S::kSubs;
+  using S = Shape<BLK, HD, PACK>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_addr(smem);
   if (base & 1023u) {                // never expected: the swizzle needs 1024-byte aligned tiles
@@ -144,25 +153,21 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t sQ = base, sK = base + S::kOffK, bar0 = base + S::kOffBar;
   const uint32_t bQFull0 = bar0, bQFree0 = bQFull0 + 8u * kQSlots, bKFull0 = bQFree0 + 8u * kQSlots,
                  bKFree0 = bKFull0 + 8u * kKSlots, bSFull0 = bKFree0 + 8u * kKSlots, bSFree0 = bSFull0 + 8u * kSBufs,
-                 bDrain = bSFree0 + 8u * kSBufs;
-  float* red = reinterpret_cast<float*>(smem + S::kOffRed);
+                 bItem0 = bSFree0 + 8u * kSBufs, bDrain = bItem0 + 8u * kItems;
+  float* negs = reinterpret_cast<float*>(smem + S::kOffNeg);
+  volatile Item* ring = reinterpret_cast<volatile Item*>(smem + S::kOffItem);
   volatile uint32_t* tmem_holder = reinterpret_cast<volatile uint32_t*>(smem + S::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kOffMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Ctl ctl{abort_flag, p.status, kWaitNs};
+  // phase x / depth of the barrier x % depth of a ring
+  auto wait = [&](uint32_t first, int depth, int x) -> bool {
+    return ctl.wait(first + 8u * (x % depth), uint32_t(x / depth) & 1u);
+  };
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kQSlots; ++s) {
-      mbar_init(bQFull0 + 8u * s, 1);
-      mbar_init(bQFree0 + 8u * s, 1);
-    }
-    for (int s = 0; s < kKSlots; ++s) {
-      mbar_init(bKFull0 + 8u * s, 1);
-      mbar_init(bKFree0 + 8u * s, 1);
-    }
-    for (int s = 0; s < kSBufs; ++s) {
-      mbar_init(bSFull0 + 8u * s, 1);
-      mbar_init(bSFree0 + 8u * s, 128);
-    }
+    for (int s = 0; s < 2 * kQSlots + 2 * kKSlots + kSBufs; ++s) mbar_init(bQFull0 + 8u * s, 1);
+    for (int s = 0; s < kSBufs; ++s) mbar_init(bSFree0 + 8u * s, 4);
+    for (int s = 0; s < kItems; ++s) mbar_init(bItem0 + 8u * s, 1);
     mbar_init(bDrain, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -178,43 +183,133 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
 
-  // Tiles are counted over all items of the CTA (t), items with k: tile t uses
-  // Q slot t % 2 and S buffer t % 4, item k the K slot k % 2.
+  // Items with kept blocks are counted by k, their tiles over all of them by t:
+  // item k uses Q slot k % 2 and ring entry k % 8, tile t K slot and S buffer t % 4.
   if (warp == 0) {
     // ================================================================ loads
-    if (lane == 0) {
-      int t = 0, k = 0;
-      bool ok = true;
-      for (int64_t it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
-        Item x;
-        if (!decode<BLK>(p, it, x)) continue;
-        if (k >= kKSlots && !(ok = ctl.wait(bKFree0 + 8u * (k % kKSlots), uint32_t(k / kKSlots - 1) & 1u))) break;
-        const uint32_t bk = bKFull0 + 8u * (k % kKSlots);
-        mbar_expect_tx(bk, S::kKBytes);
-        tma_load_kv<HD>(sK + (k % kKSlots) * S::kKBytes, &tmK, bk, x.j * BLK + x.chunk * kChunk, x.kv);
-        ++k;
-        const int tiles = (x.units + SUBS - 1) / SUBS;
-        for (int y = 0; y < tiles && ok; ++y) {
-          if (t >= kQSlots && !(ok = ctl.wait(bQFree0 + 8u * (t % kQSlots), uint32_t(t / kQSlots - 1) & 1u))) break;
-          const uint32_t bq = bQFull0 + 8u * (t % kQSlots), dst = sQ + (t % kQSlots) * S::kQBytes;
-          mbar_expect_tx(bq, S::kQBytes);
+    // An item is looked up in two steps, its row's place in the layout and then
+    // its key blocks and lse, each of them an item's time ahead of its use: done
+    // one after the other when the item comes up they take 4 us, which is the
+    // time of four tiles.
+    int k = 0, t = 0;
+    bool ok = true;
+    struct Row {
+      int unit, i, f0, e0, len;          // e0, len: still in flight until the next step
+    };
+    // unit by unit, last row first: rows grow with their index, and a unit's keys stay in L2
+    auto find_row = [&](uint32_t it) -> Row {
+      Row r{0, 0, 0, 0, -1};
+      if (it < p.items) {
+        r.unit = int(it / uint32_t(p.nb));
+        r.i = p.nb - 1 - int(it - uint32_t(r.unit) * uint32_t(p.nb));
+        r.f0 = (p.kv0 * p.upk + r.unit) * PACK;
+        const size_t at = size_t(r.f0 % p.L) * p.nb + r.i;
+        r.e0 = p.row_ptr[at];
+        r.len = p.row_ptr[at + 1];
+      }
+      return r;
+    };
+    constexpr int NQ32 = S::kNQ / 32;
+    struct Found {
+      int cols, last, base;              // lane x holds entry x; the last entry; the layout head's first
+      float lse[NQ32];
+    };
+    auto find_keys = [&](const Row& r) -> Found {
+      Found w{0, -1, 0, {}};
+      const int len = r.len - r.e0;
+      if (r.len >= 0 && len > 0) {
+        w.cols = lane < len ? p.col_idx[r.e0 + lane] : 0;
+        w.last = p.col_idx[r.e0 + len - 1];
+        w.base = p.row_ptr[size_t(r.f0 % p.L) * p.nb];
 #pragma unroll
-          for (int sub = 0; sub < SUBS; ++sub) {
-            // a tile without a second block repeats the first; its rows are left out
-            const int u = min(y * SUBS + sub, x.units - 1);
-            const int i = p.row_idx[x.e0 + u / p.hpg], f = x.f0 + u % p.hpg;
-#pragma unroll
-            for (int a = 0; a < HD / 64; ++a)
-              tma_load_3d(dst + a * S::kAtomQ + sub * BLK * 128, &tmQ, bq, a * 64, i * BLK, f);
-          }
-          ++t;
+        for (int x = 0; x < NQ32; ++x) {
+          const int c = x * 32 + lane, tok = r.i * BLK + c % BLK;
+          w.lse[x] = tok < p.n ? p.lse[size_t(r.f0 + c / BLK) * p.n + tok] : INFINITY;
         }
       }
+      return w;
+    };
+    uint32_t it = blockIdx.x;
+    Row cur = find_row(it), next = find_row(it + gridDim.x);
+    Found mine = find_keys(cur);
+    while (cur.len >= 0 && ok) {
+      it += gridDim.x;
+      const Row after = find_row(it + gridDim.x);
+      const Found theirs = find_keys(next);
+      const int e0 = cur.e0, len = cur.len - cur.e0, i = cur.i;
+      const Found w = mine;
+      const Row row = cur;
+      cur = next;
+      next = after;
+      mine = theirs;
+      if (len <= 0) continue;
+      // -lse log2 e of the item's query rows, -inf for one past the sequence's end
+      float neg[NQ32];
+      bool dead = false;
+#pragma unroll
+      for (int x = 0; x < NQ32; ++x) {
+        dead |= w.lse[x] == -INFINITY;
+        neg[x] = w.lse[x] == -INFINITY ? -INFINITY : -w.lse[x] * kLog2e;
+      }
+      dead = __any_sync(0xffffffffu, dead);
+      if (k >= kQSlots && !(ok = __all_sync(0xffffffffu, wait(bQFree0, kQSlots, k - kQSlots)))) break;
+      const int tiles = (len + S::kBPT - 1) / S::kBPT;
+#pragma unroll
+      for (int x = 0; x < NQ32; ++x) negs[(k % kItems) * 128 + x * 32 + lane] = neg[x];
+      __syncwarp();
+      if (lane == 0) {
+        volatile Item* e = ring + k % kItems;
+        e->tiles = tiles;
+        e->blocks = len;
+        e->diag = w.last == i;
+        e->dead = dead;
+        e->slot = int64_t(row.unit) * p.slots + (e0 - w.base);
+        mbar_arrive(bItem0 + 8u * (k % kItems));
+        const uint32_t bq = bQFull0 + 8u * (k % kQSlots), dst = sQ + (k % kQSlots) * S::kQBytes;
+        mbar_expect_tx(bq, S::kQBytes);
+#pragma unroll
+        for (int h = 0; h < PACK; ++h)
+#pragma unroll
+          for (int a = 0; a < HD / 64; ++a)
+            tma_load_3d(dst + a * S::kAtomQ + h * BLK * 128, &tmQ, bq, a * 64, i * BLK, row.f0 + h);
+      }
+      ++k;
+      const int kv = row.f0 / p.g;
+      int have = 0, cols = w.cols;       // lane x holds entry have + x
+      for (int y = 0; y < tiles; ++y) {
+        if (y * S::kBPT - have >= 32) {
+          have = y * S::kBPT;
+          cols = have + lane < len ? p.col_idx[e0 + have + lane] : 0;
+        }
+        if (t >= kKSlots && !(ok = __all_sync(0xffffffffu, wait(bKFree0, kKSlots, t - kKSlots)))) break;
+        // a last tile without a second block leaves that half as it was: its sums are not stored
+        const int blocks = min(S::kBPT, len - y * S::kBPT);
+        const uint32_t bk = bKFull0 + 8u * (t % kKSlots), dst = sK + (t % kKSlots) * S::kKBytes;
+        if (lane == 0) mbar_expect_tx(bk, uint32_t(blocks) * (S::kKBytes / S::kBPT));
+#pragma unroll
+        for (int x = 0; x < S::kBPT; ++x) {
+          const int j = __shfl_sync(0xffffffffu, cols, (y * S::kBPT + x - have) & 31);
+          if (lane == 0 && x < blocks) {
+#pragma unroll
+            for (int a = 0; a < HD / 64; ++a)
+              tma_load_3d(dst + a * S::kAtomK + x * BLK * 128, &tmK, bk, a * 64, j * BLK, kv);
+          }
+        }
+        ++t;
+      }
+    }
+    // the end of the stream, in an entry that the sums are done with
+    if (ok && k >= kQSlots) ok = __all_sync(0xffffffffu, wait(bQFree0, kQSlots, k - kQSlots));
+    if (lane == 0) {
+      if (ok) {
+        ring[k % kItems].tiles = 0;
+        mbar_arrive(bItem0 + 8u * (k % kItems));
+      }
       // never leave the CTA with copies in flight into its shared memory
-      for (int y = t > kQSlots ? t - kQSlots : 0; y < t; ++y)
-        wait_drain(bQFull0 + 8u * (y % kQSlots), uint32_t(y / kQSlots) & 1u, kDrainNs);
-      for (int y = k > kKSlots ? k - kKSlots : 0; y < k; ++y)
-        wait_drain(bKFull0 + 8u * (y % kKSlots), uint32_t(y / kKSlots) & 1u, kDrainNs);
+      for (int x = k > kQSlots ? k - kQSlots : 0; x < k; ++x)
+        wait_drain(bQFull0 + 8u * (x % kQSlots), uint32_t(x / kQSlots) & 1u, kDrainNs);
+      for (int x = t > kKSlots ? t - kKSlots : 0; x < t; ++x)
+        wait_drain(bKFull0 + 8u * (x % kKSlots), uint32_t(x / kKSlots) & 1u, kDrainNs);
     }
   } else if (warp == 1) {
     // ================================================================ products
@@ -222,122 +317,99 @@ __global__ void __launch_bounds__(kThreads, 2)
       constexpr uint64_t kFix = sw128_fixed(16, 1024);
       constexpr uint32_t kHi = uint32_t(kFix >> 32);
       const uint32_t q_lo = uint32_t(kFix) + (sQ >> 4), k_lo = uint32_t(kFix) + (sK >> 4);
-      int t = 0, k = 0;
       bool ok = true;
-      for (int64_t it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
-        Item x;
-        if (!decode<BLK>(p, it, x)) continue;
-        if (!(ok = ctl.wait(bKFull0 + 8u * (k % kKSlots), uint32_t(k / kKSlots) & 1u))) break;
-        const uint32_t kb = k_lo + uint32_t(k % kKSlots) * (S::kKBytes >> 4);
-        const int tiles = (x.units + SUBS - 1) / SUBS;
+      int t = 0;
+      for (int k = 0; ok; ++k) {
+        if (!(ok = wait(bItem0, kItems, k))) break;
+        const int tiles = ring[k % kItems].tiles;
+        if (tiles == 0) break;
+        if (!(ok = wait(bQFull0, kQSlots, k))) break;
+        const uint32_t qb = q_lo + uint32_t(k % kQSlots) * (S::kQBytes >> 4);
         for (int y = 0; y < tiles; ++y) {
-          if (!(ok = ctl.wait(bQFull0 + 8u * (t % kQSlots), uint32_t(t / kQSlots) & 1u))) break;
-          if (t >= kSBufs && !(ok = ctl.wait(bSFree0 + 8u * (t % kSBufs), uint32_t(t / kSBufs - 1) & 1u))) break;
+          if (!(ok = wait(bKFull0, kKSlots, t))) break;
+          if (t >= kSBufs && !(ok = wait(bSFree0, kSBufs, t - kSBufs))) break;
           tc_fence_after();
-          const uint32_t qb = q_lo + uint32_t(t % kQSlots) * (S::kQBytes >> 4);
-          const uint32_t d = tmem + (t % kSBufs) * kChunk;
+          const uint32_t kb = k_lo + uint32_t(t % kKSlots) * (S::kKBytes >> 4);
+          const uint32_t d = tmem + (t % kSBufs) * S::kNQ;
 #pragma unroll
           for (int kk = 0; kk < HD / 16; ++kk)
-            mma_ss(d, desc_from(qb + ((kk >> 2) * S::kAtomQ + (kk & 3) * 32) / 16, kHi),
-                   desc_from(kb + ((kk >> 2) * S::kAtomK + (kk & 3) * 32) / 16, kHi), S::kIdesc, kk > 0 ? 1u : 0u);
+            mma_ss(d, desc_from(kb + ((kk >> 2) * S::kAtomK + (kk & 3) * 32) / 16, kHi),
+                   desc_from(qb + ((kk >> 2) * S::kAtomQ + (kk & 3) * 32) / 16, kHi), S::kIdesc, kk > 0 ? 1u : 0u);
           tc_commit(bSFull0 + 8u * (t % kSBufs));
-          tc_commit(bQFree0 + 8u * (t % kQSlots));
+          tc_commit(bKFree0 + 8u * (t % kKSlots));
+          if (y == tiles - 1) tc_commit(bQFree0 + 8u * (k % kQSlots));
           ++t;
         }
-        if (!ok) break;
-        tc_commit(bKFree0 + 8u * (k % kKSlots));
-        ++k;
       }
       tc_commit(bDrain);
       wait_drain(bDrain, 0, kDrainNs);
     }
   } else {
-    // ================================================================ rows
-    const int q4 = warp & 3;
-    const int row = q4 * 32 + lane;
-    const int sub = row / BLK, rl = row - sub * BLK;
+    // ================================================================ sums
+    // Group t % 3 of four warps takes tile t, a key per thread; warp w reaches
+    // TMEM lanes 32 (w % 4) .., so each scheduler has a warp of every group.
+    const int q4 = warp & 3, group = (warp - 2) >> 2;
+    const int key = q4 * 32 + lane;
+    const int half = key / BLK, kl = key - half * BLK;         // key block of the tile, key in it
     const uint32_t lane_base = tmem + (uint32_t(q4 * 32) << 16);
     const float sl2 = p.scale_log2;
-    int t = 0, k = 0;
     bool ok = true;
-    for (int64_t it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
-      Item x;
-      if (!decode<BLK>(p, it, x)) continue;
-      const int tiles = (x.units + SUBS - 1) / SUBS;
-      float acc[kChunk];
-#pragma unroll
-      for (int c = 0; c < kChunk; ++c) acc[c] = 0.f;
-      // this thread's row of tile y: its query block and -lse log2 e; -inf for
-      // a row that is none or that has no weight to give
-      auto row_of = [&](int y, int& i) -> float {
-        const int u = y * SUBS + sub;
-        i = 0;
-        if (y >= tiles || u >= x.units) return -INFINITY;
-        i = p.row_idx[x.e0 + u / p.hpg];
-        const int tok = i * BLK + rl;
-        if (tok >= p.n) return -INFINITY;
-        const float lse = p.lse[size_t(x.f0 + u % p.hpg) * p.n + tok];
-        return lse == -INFINITY ? -INFINITY : -lse * kLog2e;
-      };
-      int i = 0;
-      float neg = row_of(0, i);
-      for (int y = 0; y < tiles; ++y) {
-        int i_next = 0;
-        const float neg_next = row_of(y + 1, i_next);      // fetched while this tile is worked on
-        ok = __all_sync(0xffffffffu, ctl.wait(bSFull0 + 8u * (t % kSBufs), uint32_t(t / kSBufs) & 1u));
-        if (!ok) break;
+    int t = 0;
+    for (int k = 0; ok; ++k) {
+      if (!(ok = __all_sync(0xffffffffu, wait(bItem0, kItems, k)))) break;
+      volatile Item* e = ring + k % kItems;
+      const int tiles = e->tiles;
+      if (tiles == 0) break;
+      const int y0 = (group + kGroups - t % kGroups) % kGroups;   // the item's first tile of this group
+      t += tiles;
+      if (y0 >= tiles) continue;
+      const int blocks = e->blocks, diag = e->diag ? blocks - 1 : -1, dead = e->dead;
+      float* const out = p.part + size_t(e->slot) * BLK + kl;
+      const float* const neg = negs + (k % kItems) * 128;
+      for (int y = y0; y < tiles; y += kGroups) {
+        const int tt = t - tiles + y;
+        const uint32_t s_col = lane_base + (tt % kSBufs) * S::kNQ;
+        if (!(ok = __all_sync(0xffffffffu, wait(bSFull0, kSBufs, tt)))) break;
         tc_fence_after();
-        float sv[kChunk];
-        const uint32_t s_col = lane_base + (t % kSBufs) * kChunk;
-        tmem_ld32(s_col, sv);
-        tmem_ld32(s_col + 32, sv + 32);
-        tmem_wait_ld();
-        tc_fence_before();
-        mbar_arrive(bSFree0 + 8u * (t % kSBufs));
-        ++t;
-        if (neg != -INFINITY) {
-          if (i == x.j) {
-            // the diagonal block: keys up to the row's own token
-            const int lim = rl - x.chunk * kChunk;
+        const int blk = y * S::kBPT + half;                    // the thread's kept block
+        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+        float sv[2][32];
+        tmem_ld32(s_col, sv[0]);
 #pragma unroll
-            for (int c = 0; c < kChunk; ++c)
-              if (c <= lim) acc[c] += ex2(fmaf(sv[c], sl2, neg));
+        for (int c0 = 0; c0 < S::kNQ; c0 += 32) {
+          float* const v = sv[c0 / 32 & 1];
+          wait_ld32(v);
+          if (c0 + 32 < S::kNQ) {
+            tmem_ld32(s_col + c0 + 32, sv[(c0 / 32 & 1) ^ 1]);   // while these columns are worked on
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bSFree0 + 8u * (tt % kSBufs));
+          }
+          if (dead || blk == diag) {
+            // the diagonal block takes queries from the key's own token on; a
+            // query row without weight gives nothing, whatever its scores are
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const float n = neg[c0 + c];
+              const bool use = (blk != diag || (c0 + c) % BLK >= kl) && n != -INFINITY;
+              const float x = ex2(fmaf(v[c], sl2, n));
+              s0 += use ? x : 0.f;
+            }
           } else {
 #pragma unroll
-            for (int c = 0; c < kChunk; c += 2) {
-              float x0, x1;
-              fma2(x0, x1, sv[c], sv[c + 1], sl2, neg);
-              add2(acc[c], acc[c + 1], ex2(x0), ex2(x1));
+            for (int c = 0; c < 32; c += 4) {
+              const float4 n = *reinterpret_cast<const float4*>(neg + c0 + c);
+              float x0, x1, x2, x3;
+              fma2(x0, x1, v[c], v[c + 1], sl2, n.x, n.y);
+              fma2(x2, x3, v[c + 2], v[c + 3], sl2, n.z, n.w);
+              add2(s0, s1, ex2(x0), ex2(x1));
+              add2(s2, s3, ex2(x2), ex2(x3));
             }
           }
         }
-        neg = neg_next;
-        i = i_next;
+        if (blk < blocks) out[size_t(blk) * BLK] = (s0 + s1) + (s2 + s3);
       }
-      if (!ok) break;
-      // 64 sums over the warp's 32 rows: lanes hand half of their columns over
-      // at each step, and end with the sums of columns 2 lane and 2 lane + 1
-#pragma unroll
-      for (int half = kChunk / 2, off = 16; off > 0; half /= 2, off /= 2) {
-        const bool high = lane & off;
-#pragma unroll
-        for (int c = 0; c < kChunk / 2; ++c) {
-          if (c < half) {
-            const float give = high ? acc[c] : acc[c + half];
-            const float keep = high ? acc[c + half] : acc[c];
-            acc[c] = keep + __shfl_xor_sync(0xffffffffu, give, off);
-          }
-        }
-      }
-      float* to = red + (k & 1) * 4 * kChunk;
-      *reinterpret_cast<float2*>(to + q4 * kChunk + 2 * lane) = make_float2(acc[0], acc[1]);
-      // two buffers in turn: a warp that writes one again has passed the
-      // barrier of the item between, after every read of it
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      if (row < kChunk)
-        p.part[x.slot * BLK + x.chunk * kChunk + row] =
-            (to[row] + to[kChunk + row]) + (to[2 * kChunk + row] + to[3 * kChunk + row]);
-      ++k;
     }
   }
   tc_fence_before();
@@ -348,46 +420,81 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// w[kv][u] += the runs of u's block, query head by query head and run by run.
+// w[kv][u] += the sums of u's block, unit by unit and row by row.  A block of
+// 1024 threads takes the SL = 1024 / B key blocks j0 .. j0 + SL - 1, a slice of
+// B threads for each; a column of more than kLong rows (a global first block's)
+// is shared out over all slices.
+constexpr int kAddThreads = 1024, kLong = 64;
 template <int BLK>
-__global__ void __launch_bounds__(BLK) add_runs_kernel(const Params p) {
-  const int kv = blockIdx.x / p.nb, j = blockIdx.x - kv * p.nb;
-  const int u = j * BLK + threadIdx.x;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (u >= p.n) return;
-  // a wait that ran out left runs unwritten: nothing is added then
-  if (*reinterpret_cast<volatile uint32_t*>(p.status) & kStatusTimeout) return;
+__global__ void __launch_bounds__(kAddThreads) add_rows_kernel(const Params p) {
+  constexpr int SL = kAddThreads / BLK;
+  __shared__ int s_col[SL + 1];
+  __shared__ float s_sum[kAddThreads];
+  const int per = (p.nb + SL - 1) / SL;
+  const int kvl = blockIdx.x / per, j0 = (blockIdx.x - kvl * per) * SL;
+  const int sl = threadIdx.x / BLK, kl = threadIdx.x % BLK;
+  const int u = (j0 + sl) * BLK + kl;
   float sum = 0.f;
-  for (int h = 0; h < p.g; h += p.hpg) {
-    const int f = kv * p.g + h, lh = f % p.L;
-    const int c0 = p.col_ptr[size_t(lh) * p.nb + j], c1 = p.col_ptr[size_t(lh) * p.nb + j + 1];
-    const int runs = (c1 - c0 + kColumnSegment - 1) / kColumnSegment;
-    const size_t slot = size_t(f / p.hpg) * p.slots +
-                        (c0 / kColumnSegment - p.col_ptr[size_t(lh) * p.nb] / kColumnSegment) + j;
-    const float* src = p.part + slot * BLK + threadIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");     // the sums are in memory from here on
+  for (int x0 = 0; x0 < p.upk; ++x0) {
+    const int unit = kvl * p.upk + x0;
+    const int lh = (p.kv0 * p.upk + unit) * p.pack % p.L;
+    const size_t h0 = size_t(lh) * p.nb;
+    const float* const src = p.part + (int64_t(unit) * p.slots - p.row_ptr[h0]) * BLK + kl;
+    __syncthreads();
+    if (threadIdx.x <= SL) s_col[threadIdx.x] = p.col_ptr[h0 + min(j0 + int(threadIdx.x), p.nb)];
+    __syncthreads();
+    // the sums of entries c, c + step, .. below c1, in this order
+    auto add = [&](int c, int c1, int step) {
+      float t = 0.f;
 #pragma unroll 8
-    for (int r = 0; r < runs; ++r) sum += src[size_t(r) * BLK];
+      for (; c < c1; c += step) t += src[int64_t(p.csr_pos[c]) * BLK];
+      return t;
+    };
+    const int c0 = s_col[sl], c1 = s_col[sl + 1];
+    if (c1 - c0 <= kLong) sum += add(c0, c1, 1);
+    for (int x = 0; x < SL; ++x) {
+      const int d0 = s_col[x], d1 = s_col[x + 1];
+      if (d1 - d0 <= kLong) continue;
+      __syncthreads();
+      s_sum[threadIdx.x] = add(d0 + sl, d1, SL);
+      __syncthreads();
+      if (sl == x)
+        for (int y = 0; y < SL; ++y) sum += s_sum[y * BLK + kl];
+    }
   }
-  p.weights[size_t(kv) * p.weights_stride + u] += sum;
+  // a wait that ran out left sums unwritten: nothing is added then
+  if (u >= p.n || (*reinterpret_cast<volatile uint32_t*>(p.status) & kStatusTimeout)) return;
+  p.weights[size_t(p.kv0 + kvl) * p.weights_stride + u] += sum;
 }
 
-// Partial-sum rows of a head group: the most that a layout head's runs name.
-int slots_of(const bsa_layout* L) {
-  int most = 1;
-  for (int h = 0; h < L->L; ++h) {
-    const int a = L->col_ptr[size_t(h) * L->nb], b = L->col_ptr[size_t(h + 1) * L->nb];
-    most = std::max(most, b / kColumnSegment - a / kColumnSegment + L->nb + 1);
-  }
+// Query heads of a unit: two for B = 64 when a group's heads pair off on one route.
+int pack_of(const bsa_layout* L, int g) { return L->B == 64 && g % 2 == 0 && L->L == 1 ? 2 : 1; }
+
+// Kept blocks that a unit needs room for: the most of any layout head.
+int64_t kept_of(const bsa_layout* L) {
+  int64_t most = 1;
+  for (int h = 0; h < L->L; ++h)
+    most = std::max<int64_t>(most, L->row_ptr[size_t(h + 1) * L->nb] - L->row_ptr[size_t(h) * L->nb]);
   return most;
 }
 
-template <int BLK, int HD>
-int launch(const void* q, const void* k, int heads, Params p, cudaStream_t stream) {
-  using S = Shape<BLK, HD>;
-  auto kern = prompt_weights_kernel<BLK, HD>;
-  // enough shared memory that no third CTA shares an SM: TMEM holds two
-  constexpr int smem = S::kSmem < 77 * 1024 ? 77 * 1024 : S::kSmem;
-  static_assert(2 * (smem + 1024) <= 228 * 1024, "two CTAs per SM");
+// Key/value heads of a strip: as many as kStripBytes hold, at least one.
+int strip_of(const bsa_layout* L, int heads, int kv_heads) {
+  const int upk = heads / kv_heads / pack_of(L, heads / kv_heads);
+  const size_t one = size_t(kept_of(L)) * upk * L->B * sizeof(float);
+  return int(std::max<size_t>(1, std::min<size_t>(kv_heads, kStripBytes / one)));
+}
+
+size_t bytes_of(const bsa_layout* L, int heads, int kv_heads) {
+  const int upk = heads / kv_heads / pack_of(L, heads / kv_heads);
+  return size_t(strip_of(L, heads, kv_heads)) * upk * size_t(kept_of(L)) * L->B * sizeof(float);
+}
+
+template <int BLK, int HD, int PACK>
+int launch(const void* q, const void* k, int kv_heads, Params p, const bsa_layout* layout, cudaStream_t stream) {
+  using S = Shape<BLK, HD, PACK>;
+  auto kern = prompt_weights_kernel<BLK, HD, PACK>;
   static std::mutex mu;
   static int sms[64] = {};
   int dev = 0, n_sm = 0;
@@ -396,7 +503,7 @@ int launch(const void* q, const void* k, int heads, Params p, cudaStream_t strea
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!sms[dev]) {
-      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
       if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
       if (e != cudaSuccess) return set_error(BSA_ERR_CUDA, std::string("weights attributes: ") + cudaGetErrorString(e));
       sms[dev] = n_sm;
@@ -404,25 +511,29 @@ int launch(const void* q, const void* k, int heads, Params p, cudaStream_t strea
     n_sm = sms[dev];
   }
   CUtensorMap mq, mk;
-  int st = tmap::encode_atoms(&mq, q, heads, p.n, HD, BLK);
-  if (st == BSA_OK) st = tmap::encode_kv(&mk, k, p.kv_heads, p.n, HD);
+  int st = tmap::encode_atoms(&mq, q, p.heads, p.n, HD, BLK);
+  if (st == BSA_OK) st = tmap::encode_atoms(&mk, k, kv_heads, p.n, HD, BLK);
   if (st != BSA_OK) return st;
-  p.items = int64_t(p.groups) * p.max_segs * S::kCPB;
-  const unsigned grid = unsigned(std::min<int64_t>(p.items, 2 * n_sm));
-  kern<<<grid, kThreads, smem, stream>>>(mq, mk, p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return set_error(BSA_ERR_CUDA, std::string("prompt weights launch: ") + cudaGetErrorString(e));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(p.kv_heads) * unsigned(p.nb), 1, 1);
-  cfg.blockDim = dim3(BLK, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, add_runs_kernel<BLK>, p);
-  if (e != cudaSuccess) return set_error(BSA_ERR_CUDA, std::string("weights sum launch: ") + cudaGetErrorString(e));
+  const int strip = strip_of(layout, p.heads, kv_heads);
+  for (p.kv0 = 0; p.kv0 < kv_heads; p.kv0 += strip) {
+    p.kvs = std::min(strip, kv_heads - p.kv0);
+    p.items = uint32_t(p.kvs) * uint32_t(p.upk) * uint32_t(p.nb);
+    kern<<<std::min(p.items, unsigned(n_sm)), kThreads, S::kSmem, stream>>>(mq, mk, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return set_error(BSA_ERR_CUDA, std::string("prompt weights launch: ") + cudaGetErrorString(e));
+    cudaLaunchConfig_t cfg = {};
+    constexpr int SL = kAddThreads / BLK;
+    cfg.gridDim = dim3(unsigned(p.kvs) * unsigned((p.nb + SL - 1) / SL), 1, 1);
+    cfg.blockDim = dim3(kAddThreads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, add_rows_kernel<BLK>, p);
+    if (e != cudaSuccess) return set_error(BSA_ERR_CUDA, std::string("weights sum launch: ") + cudaGetErrorString(e));
+  }
   return BSA_OK;
 }
 
@@ -436,10 +547,6 @@ int check_sizes(const bsa_layout* layout, int heads, int kv_heads) {
   if (heads % layout->L) return set_error(BSA_ERR_SHAPE, "heads must be a multiple of layout_heads");
   if (int64_t(heads) * layout->nb > INT32_MAX) return set_error(BSA_ERR_SHAPE, "too many (head, block) work items");
   return BSA_OK;
-}
-
-size_t bytes_of(const bsa_layout* layout, int heads, int kv_heads) {
-  return size_t(layout->L == 1 ? kv_heads : heads) * slots_of(layout) * layout->B * sizeof(float);
 }
 
 }  // namespace wts
@@ -472,14 +579,14 @@ int bsa_attention_weights(const void* q, const void* k, const float* lse, const 
   if (workspace_bytes < need)
     return set_error(BSA_ERR_SHAPE, "workspace too small: " + std::to_string(need) + " bytes needed");
   st = check_layout_device(layout);
-  if (st != BSA_OK || layout->max_segs < 1) return st;   // no runs: an explicit mask that keeps no block
+  if (st != BSA_OK || layout->col_idx.empty()) return st;   // no kept block, no weight
   st = tmap::get_encoder();
   if (st != BSA_OK) return st;
   wts::Params p{};
+  p.row_ptr = layout->d_row_ptr;
+  p.col_idx = layout->d_col_idx;
   p.col_ptr = layout->d_col_ptr;
-  p.row_idx = layout->d_row_idx;
-  p.seg_ptr = layout->d_seg_ptr;
-  p.segs = layout->d_segs;
+  p.csr_pos = layout->d_csr_pos;
   p.lse = lse;
   p.part = static_cast<float*>(workspace);
   p.weights = weights;
@@ -489,15 +596,22 @@ int bsa_attention_weights(const void* q, const void* k, const float* lse, const 
   p.nb = layout->nb;
   p.L = layout->L;
   p.g = heads / kv_heads;
-  p.kv_heads = kv_heads;
-  p.hpg = layout->L == 1 ? p.g : 1;
-  p.groups = heads / p.hpg;
-  p.max_segs = layout->max_segs;
-  p.slots = wts::slots_of(layout);
+  p.heads = heads;
+  p.pack = wts::pack_of(layout, p.g);
+  p.upk = p.g / p.pack;
+  p.slots = wts::kept_of(layout);
   p.scale_log2 = float(double(scale) * 1.4426950408889634);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (B == 64) return d == 128 ? wts::launch<64, 128>(q, k, heads, p, s) : wts::launch<64, 64>(q, k, heads, p, s);
-  return d == 128 ? wts::launch<128, 128>(q, k, heads, p, s) : wts::launch<128, 64>(q, k, heads, p, s);
+  if (B == 128) {
+    return d == 128 ? wts::launch<128, 128, 1>(q, k, kv_heads, p, layout, s)
+                    : wts::launch<128, 64, 1>(q, k, kv_heads, p, layout, s);
+  }
+  if (p.pack == 2) {
+    return d == 128 ? wts::launch<64, 128, 2>(q, k, kv_heads, p, layout, s)
+                    : wts::launch<64, 64, 2>(q, k, kv_heads, p, layout, s);
+  }
+  return d == 128 ? wts::launch<64, 128, 1>(q, k, kv_heads, p, layout, s)
+                  : wts::launch<64, 64, 1>(q, k, kv_heads, p, layout, s);
 }
 
 }  // extern "C"

@@ -266,9 +266,12 @@ int bsa_decode(const void* q, const void* k_cache, const void* v_cache,
                int heads, int kv_heads, int d, float scale, void* o, float* lse,
                void* stream);
 
-/* Bytes of device workspace bsa_attention_weights needs: partial sums of the
- * column runs of every key block, fp32.  Depends on the layout (a host-only one
- * will do), not on d.  0 for sizes the call would refuse. */
+/* Bytes of device workspace bsa_attention_weights needs: the sums of every kept
+ * block, B floats per query head (per two heads where B = 64 and the heads of
+ * a group pair off on one route), of as many key/value heads as 64 MiB hold,
+ * at least one.
+ * Depends on the layout (a host-only one will do), not on d.  0 for sizes the
+ * call would refuse. */
 size_t bsa_attention_weights_workspace_bytes(const bsa_layout* layout, int heads, int kv_heads);
 
 /* The attention weight that every key of a prompt has received, added to
@@ -285,8 +288,8 @@ size_t bsa_attention_weights_workspace_bytes(const bsa_layout* layout, int heads
  * fixes, so a call gives the same bits every time.  Requirements (checked
  * before launch; errors launch nothing): as for bsa_forward; workspace
  * 16-byte aligned and of at least the bytes above, used by no other call at
- * the same time.  Enqueues two kernels (none for an explicit mask that keeps
- * no block) and returns; no allocation. */
+ * the same time.  Enqueues two kernels for every 64 MiB of kept blocks' sums
+ * (none for a layout that keeps nothing) and returns; no allocation. */
 int bsa_attention_weights(const void* q, const void* k, const float* lse,
                           const bsa_layout* layout, int B, int n, int heads, int kv_heads,
                           int d, float scale, float* weights, size_t weights_stride,

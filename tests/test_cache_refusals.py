@@ -112,19 +112,10 @@ def test_workspace_sizes(lay):
     h = lay.handle
     assert bsa.bsa_attention_weights_workspace_bytes(0, 8, 4) == 0
     assert bsa.bsa_attention_weights_workspace_bytes(h, 6, 4) == 0
-    col_ptr, _ = bsa.bsa_layout_csc(h)
-    nb = len(col_ptr) // 2
-    slots = max(col_ptr[(x + 1) * nb] // 16 - col_ptr[x * nb] // 16 for x in range(2)) + nb + 1
-    assert bsa.bsa_attention_weights_workspace_bytes(h, 8, 4) == 8 * slots * B * 4
-    # every run of a column has a row of its own among them
-    for x in range(2):
-        seen = set()
-        for j in range(nb):
-            c0, c1 = col_ptr[x * nb + j], col_ptr[x * nb + j + 1]
-            for e in range(c0, c1, 16):
-                slot = e // 16 - col_ptr[x * nb] // 16 + j
-                assert slot not in seen and 0 <= slot < slots
-                seen.add(slot)
+    row_ptr, _ = bsa.bsa_layout_csr(h)
+    nb = len(row_ptr) // 2
+    kept = max(row_ptr[nb] - row_ptr[0], row_ptr[2 * nb] - row_ptr[nb])
+    assert bsa.bsa_attention_weights_workspace_bytes(h, 8, 4) == 8 * kept * B * 4
     assert bsa.bsa_evict_workspace_bytes(h, 2, 4, 0) == 0
     assert bsa.bsa_evict_workspace_bytes(h, 2, 4, 100) >= 4 * 100 * 4 * 2
     # a budget past the layout's tokens needs no more than one of all of them
@@ -134,6 +125,16 @@ def test_workspace_sizes(lay):
     assert bsa.bsa_decode_tree_workspace_bytes(h, 2, 8, 4, 129, 64) == 0
     small, large = (bsa.bsa_decode_tree_workspace_bytes(h, 2, 8, 4, T, 64) for T in (1, 128))
     assert 0 < small < large
+
+
+def test_prompt_weights_take_as_many_heads_at_a_time_as_64_mib_hold():
+    n = 64 * 600
+    for heads, kv, units in ((8, 4, 1), (9, 3, 3), (2, 2, 1)):
+        full = bsa.Layout(OL.BAND_GLOBAL, n, 64, 1, -1, window=600, global_first=0)
+        one = units * (600 * 601 // 2) * 64 * 4
+        need = bsa.bsa_attention_weights_workspace_bytes(full.handle, heads, kv)
+        assert need == max(1, min(kv, (64 << 20) // one)) * one
+        full.close()
 
 
 def test_sizes_that_pass_32_bits_are_refused_not_wrapped(lay):

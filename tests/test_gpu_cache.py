@@ -139,6 +139,27 @@ def test_prompt_weights(case):
     lay.close()
 
 
+def test_prompt_weights_in_strips():
+    """So many kept blocks that key/value heads take the workspace in turns: some columns against fp64, all by
+    their total (every query row gives one)."""
+    n, B, H, G, d = 64 * 600, 64, 8, 4, 64
+    lay = _layout(OL.BAND_GLOBAL, n, B, 1, dict(window=n // B, global_first=0))
+    assert (600 * 601 // 2) * B * 4 > (64 << 20) // 2               # one key/value head at a time
+    q, k, v = (to_device_bf16(x) for x in inputs.qkv_bits(H, G, n, d, seeds=(7, 8, 9)))
+    _, lse = bsa.attention(q, k, v, lay)
+    w, w2 = bsa.attention_weights(q, k, lse, lay), bsa.attention_weights(q, k, lse, lay)
+    torch.cuda.synchronize()
+    bsa.bsa_get_status(lay.handle)
+    assert torch.equal(w, w2)
+    # a score is off by e_s <= 2e-5 here (norms up to 11), a row's sum of terms by no more, and lse by 2^-23 of it
+    assert float((w.double().sum(1) / n - H // G).abs().max()) <= H // G * 3e-5
+    for u in (0, 5, 63, 64, 19200, 30001, n - 1):
+        x = (q[:, u:].double() * k.repeat_interleave(2, 0)[:, u:u + 1].double()).sum(-1) * d ** -0.5
+        want = torch.exp(x - lse[:, u:].double()).sum(-1).view(G, 2).sum(1)
+        assert float(((w[:, u].double() - want) / want).abs().max()) <= 3e-5
+    lay.close()
+
+
 def test_prompt_weights_of_rows_that_are_not_numbers_stay_in_their_columns():
     """A NaN or infinite query row reaches only the keys it may read; rows with lse = -inf give nothing;
     a NaN key only its own column."""
