@@ -90,24 +90,23 @@ __device__ __forceinline__ int ld_peer(uint32_t a) {
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
-__device__ __forceinline__ int4 ld_peer4(uint32_t a) {
-  int4 v;
-  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a)
-               : "memory");
-  return v;
+__device__ __forceinline__ void add_peer(uint32_t a, int v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 
 // A cluster of C blocks per row; block r owns the slots [r per, (r + 1) per).
-// What the blocks have to know of each other (the newest token, a digit's
-// histogram, the holes and movers before a block) each reads from the others'
-// shared memory after a barrier, and nothing read so is written again.
+// Each block adds the bins that it has keys in (few: the keys under one prefix
+// share their upper bits) to every block's sum of histograms; the newest
+// token, ties, holes and movers before it a block reads from the others' shared
+// memory after a barrier.  Nothing read so is written again.  The loops are not
+// unrolled: a block runs through them once or a few times, and fetching their
+// instructions is what it would wait for.
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int C) {
   extern __shared__ uint32_t s_keys[];
-  __shared__ __align__(16) int hist[3][kBins];
+  __shared__ __align__(16) int hist[kBins];       // this block's
+  __shared__ __align__(16) int sums[3][kBins];    // the cluster's, a digit each
   __shared__ int s_scan[3][kSelWarps];
-  __shared__ int s_bad, s_newest, s_digit, s_left, s_holes, s_movers;
+  __shared__ int s_bad, s_newest, s_digit, s_left, s_equal, s_holes, s_movers;
   grid_release();
   const int row = blockIdx.x / C, rank = cluster_rank();
   const int b = row / p.hkv;
@@ -129,9 +128,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
     }
     if (bad) s_bad = 1;
   }
+  reinterpret_cast<int4*>(hist)[tid] = make_int4(0, 0, 0, 0);
 #pragma unroll
-  for (int d = 0; d < 3; ++d)
-    for (int x = tid; x < kBins; x += kSelThreads) hist[d][x] = 0;
+  for (int d = 0; d < 3; ++d) reinterpret_cast<int4*>(sums[d])[tid] = make_int4(0, 0, 0, 0);
   __syncthreads();
   if (s_bad) {
     if (tid == 0 && rank == 0) {
@@ -155,8 +154,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
     }
     m = __reduce_max_sync(0xffffffffu, m);
     if (lane == 0) atomicMax(&s_newest, m);
-    cluster_sync();
+    cluster_sync();                      // also: every block's sums are zero from here on
     newest = INT32_MIN;
+#pragma unroll 1
     for (int r = 0; r < C; ++r) newest = max(newest, ld_peer(peer_addr(&s_newest, r)));
     if (len == 0) newest = -1;
   }
@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
     cluster_sync();                      // the others may still be reading s_newest here
     return;
   }
+  if (!tok && C > 1) cluster_sync();     // every block's sums are zero
   const int64_t floor_tok = int64_t(newest) - p.recent;      // tokens above it are protected
   auto key_from = [&](int t, float x) -> uint32_t { return int64_t(t) > floor_tok ? 0xffffffffu : key_of(x); };
   auto make_key = [&](int s) -> uint32_t { return key_from(tok ? tok[s] : s, w[s]); };
@@ -189,37 +190,42 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
   // ---- the budget-th largest key, from the highest digit down
   uint32_t prefix = 0, mask = 0;
   int left = p.budget;                   // how many of the keys under the prefix are kept
-  int ties0 = 0;                         // keys equal to the last one, in the blocks before this one
-  constexpr int kShift[3] = {21, 10, 0}, kBits[3] = {11, 11, 10};
-#pragma unroll
+#pragma unroll 1
   for (int d = 0; d < 3; ++d) {
-    const uint32_t dm = (1u << kBits[d]) - 1u;
+    const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
+    const uint32_t dm = d == 2 ? 1023u : 2047u;
+#pragma unroll 1
     for (int s0 = first; s0 < end; s0 += kSelThreads) {
       const int s = s0 + tid;            // a thread reads the keys that it wrote
       const uint32_t k = s < end ? key_at(s) : 0u;
       const bool in = s < end && (k & mask) == prefix;
-      const int bin = in ? int(k >> kShift[d] & dm) : -1;
+      const int bin = in ? int(k >> shift & dm) : -1;
       // one bin for the whole warp (a run of equal weights) is one addition
       int same;
       __match_all_sync(0xffffffffu, bin, &same);
       if (same) {
-        if (lane == 0 && bin >= 0) atomicAdd(&hist[d][bin], 32);
+        if (lane == 0 && bin >= 0) atomicAdd(&hist[bin], 32);
       } else if (in) {
-        atomicAdd(&hist[d][bin], 1);
+        atomicAdd(&hist[bin], 1);
       }
     }
-    cluster_sync();
-    // the digit whose keys, counted from above, reach `left`: each thread owns
-    // four bins of the cluster's sum, thread 0 the highest ones
+    __syncthreads();
+    // each thread owns four bins, thread 0 the highest ones
     const int top = kBins - 4 - 4 * tid;
-    int4 c = make_int4(0, 0, 0, 0);
-    for (int r = 0; r < C; ++r) {
-      const int4 x = ld_peer4(peer_addr(&hist[d][top], r));
-      c.x += x.x;
-      c.y += x.y;
-      c.z += x.z;
-      c.w += x.w;
+    int4 c = *reinterpret_cast<const int4*>(&hist[top]);
+    if (C > 1) {
+      const int own4[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (own4[x])
+#pragma unroll 1
+          for (int r = 0; r < C; ++r) add_peer(peer_addr(&sums[d][top + x], r), own4[x]);
+      cluster_sync();
+      c = *reinterpret_cast<const int4*>(&sums[d][top]);
     }
+    // the last digit's own counts are read by the other blocks
+    if (d < 2) *reinterpret_cast<int4*>(&hist[top]) = make_int4(0, 0, 0, 0);
+    // the digit whose keys, counted from above, reach `left`
     const int own = c.x + c.y + c.z + c.w;
     int sum = own;
 #pragma unroll
@@ -229,29 +235,23 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
     }
     if (lane == 31) s_scan[d][warp] = sum;
     __syncthreads();
-    for (int x = 0; x < warp; ++x) sum += s_scan[d][x];
+    // sums of the warps before, by the lanes
+    sum += __reduce_add_sync(0xffffffffu, lane < warp ? s_scan[d][lane & (kSelWarps - 1)] : 0);
     int above = sum - own;               // keys in higher bins than the thread's
     if (above < left && left <= sum) {
       const int bin[4] = {c.w, c.z, c.y, c.x};
-      int digit = top + 3;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        if (above + bin[x] >= left) break;
-        above += bin[x];
-        --digit;
-      }
-      s_digit = digit;
+      int x = 0;
+      while (above + bin[x] < left) above += bin[x++];
+      s_digit = top + 3 - x;
       s_left = left - above;
+      s_equal = bin[x];
     }
     __syncthreads();
-    const int digit = s_digit;
-    prefix |= uint32_t(digit) << kShift[d];
-    mask |= dm << kShift[d];
+    prefix |= uint32_t(s_digit) << shift;
+    mask |= dm << shift;
     left = s_left;
-    if (d == 2)
-      for (int r = 0; r < rank; ++r) ties0 += ld_peer(peer_addr(&hist[d][digit], r));
-    __syncthreads();
   }
+  const bool split = s_equal > left;     // some keys equal to the last one stay, some go
   // keys above `prefix` are kept, and of those equal to it the first `left`
 
   // ---- ranks: each warp owns a run of the block's slots
@@ -261,20 +261,22 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
   auto before = [&](int* scan, int count, int& total) -> int {
     if (lane == 0) scan[warp] = count;
     __syncthreads();
-    int pre = 0;
-    total = 0;
-    for (int x = 0; x < kSelWarps; ++x) {
-      if (x < warp) pre += scan[x];
-      total += scan[x];
-    }
-    return pre;
+    const int v = scan[lane & (kSelWarps - 1)];
+    total = __reduce_add_sync(0xffffffffu, lane < kSelWarps ? v : 0);
+    return __reduce_add_sync(0xffffffffu, lane < warp ? v : 0);
   };
-  int count = 0, total = 0;
-  for (int s0 = lo; s0 < hi; s0 += 32) {
-    const int s = s0 + lane;
-    count += __popc(__ballot_sync(0xffffffffu, s < hi && key_at(s) == prefix));
+  int total = 0, ties = 0;
+  if (split) {
+#pragma unroll 1
+    for (int r = 0; r < rank; ++r) ties += ld_peer(peer_addr(&hist[prefix & 1023u], r));
+    int count = 0;
+#pragma unroll 1
+    for (int s0 = lo; s0 < hi; s0 += 32) {
+      const int s = s0 + lane;
+      count += __popc(__ballot_sync(0xffffffffu, s < hi && key_at(s) == prefix));
+    }
+    ties += before(s_scan[0], count, total);
   }
-  const int ties = ties0 + before(s_scan[0], count, total);
   // kept slots of a ballot, with the ties seen so far
   auto kept_of = [&](int s0, int& seen) -> unsigned {
     const int s = s0 + lane;
@@ -285,6 +287,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
     return __ballot_sync(0xffffffffu, take);
   };
   int holes = 0, movers = 0, seen = ties;
+#pragma unroll 1
   for (int s0 = lo; s0 < hi; s0 += 32) {
     const unsigned kept = kept_of(s0, seen);
     // slots of this ballot that lie below the budget
@@ -298,6 +301,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
   int mover0 = before(s_scan[2], movers, total);
   if (tid == 0) s_movers = total;
   cluster_sync();
+#pragma unroll 1
   for (int r = 0; r < rank; ++r) {
     hole0 += ld_peer(peer_addr(&s_holes, r));
     mover0 += ld_peer(peer_addr(&s_movers, r));
@@ -305,6 +309,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
   int32_t* const mv = p.movers + size_t(row) * p.cap;
   int32_t* const src = p.src + size_t(row) * p.cap;
   seen = ties;
+#pragma unroll 1
   for (int s0 = lo; s0 < hi; s0 += 32) {
     const unsigned kept = kept_of(s0, seen);
     const int s = s0 + lane;
@@ -422,9 +427,9 @@ int launch(const Params& p, int rows, int d, cudaStream_t stream) {
     }
   }
   // blocks per row: one for each kSlotsPerBlock slots, so that a thread has one
-  // batch of them
+  // batch of them, while the GPU holds them two to an SM
   int C = 1;
-  while (C < kMaxCluster && p.n > C * kSlotsPerBlock) C *= 2;
+  while (C < kMaxCluster && p.n > C * kSlotsPerBlock && rows * C <= 148) C *= 2;
   const int per = (p.n + C * 32 - 1) / (C * 32) * 32;
   cudaLaunchConfig_t sel = {};
   sel.gridDim = dim3(unsigned(rows) * unsigned(C), 1, 1);

@@ -659,21 +659,21 @@ __device__ __forceinline__ int find_block(const Params& p, size_t at, int j) {
 }
 
 // The step: blocks [0, row_blocks) join one row per warp; the others turn the
-// scores of kTileKeys list keys of a key/value head into weights, four keys a
-// thread (one block a 256 keys spent its time on finding M and L: 82 us for
-// the 16 x 16K step, against 23 so).
-constexpr int kTileKeys = 4 * kJoinWarps * 32;
+// scores of kTileKeys list keys of a key/value head into weights, kGroups
+// times four keys a thread.  (With 256 keys a block the 16 x 16K step spent
+// 82 us here, most of it on finding M and L again.)
+constexpr int kGroups = 4, kGroupKeys = 4 * kJoinWarps * 32, kTileKeys = kGroups * kGroupKeys;
 
 template <int BLK, int HD>
-__global__ void __launch_bounds__(kJoinWarps * 32, 1) join_step_kernel(const Params p, int heads, int row_blocks) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 3) join_step_kernel(const Params p, int heads, int row_blocks) {
   __shared__ float s_m[32], s_l[32];
   __shared__ int s_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  grid_wait();
   if (int(blockIdx.x) < row_blocks) {
     const int f = blockIdx.x * kJoinWarps + warp;
+    const int b = min(f, heads - 1) / p.H, t = p.lengths[b];
+    grid_wait();
     if (f >= heads) return;
-    const int b = f / p.H, t = p.lengths[b];
     const bool in = t >= 0 && t < p.n;
     float M = -INFINITY, L = 0.f, acc[HD / 32] = {};
     int flag = 0;
@@ -695,25 +695,34 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 1) join_step_kernel(const Par
   const int g = p.H / p.hkv;
   const int b = hg / p.hg, h0 = (hg - b * p.hg) * p.hpt;    // the block's query head(s) in the sequence
   const int t = p.lengths[b];
-  if (t < 0 || t >= p.n) return;
-  const size_t at0 = size_t((b * p.H + h0) % p.L) * p.nb + t / BLK;
-  const int start = p.row_ptr[at0], list = (p.row_ptr[at0 + 1] - start) * BLK;
-  if (tile * kTileKeys >= list) return;
+  const bool in = t >= 0 && t < p.n;
+  const size_t at0 = size_t((b * p.H + h0) % p.L) * p.nb + (in ? t / BLK : 0);
+  const int start = p.row_ptr[at0], list = in ? (p.row_ptr[at0 + 1] - start) * BLK : 0;
   const int kv = h0 / g, first = p.L == 1 ? h0 : kv * g;    // first query head of the group
-  const int k0 = tile * kTileKeys + threadIdx.x * 4;        // four keys of one block
-  const int j = k0 < list ? p.col_idx[start + k0 / BLK] : -1;
-  const int u = j * BLK + k0 % BLK;
-  bool mine = j >= 0 && u <= t;
-  float* const to = p.weights + size_t(b * p.hkv + kv) * p.weights_stride + u;
-  float sum[4] = {0.f, 0.f, 0.f, 0.f}, old[4];
+  float* const w = p.weights + size_t(b * p.hkv + kv) * p.weights_stride;
+  // what needs no result of kernel 1 comes before the wait for it
+  int u[kGroups];                                           // first of four keys; past t if there are none
+  float old[kGroups][4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) old[e] = mine && u + e <= t ? to[e] : 0.f;
+  for (int i = 0; i < kGroups; ++i) {
+    const int k = tile * kTileKeys + i * kGroupKeys + int(threadIdx.x) * 4;
+    u[i] = k < list ? p.col_idx[start + k / BLK] * BLK + k % BLK : INT32_MAX;
+  }
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) old[i][e] = u[i] <= t && u[i] + e <= t ? w[u[i] + e] : 0.f;
+  grid_wait();
+  if (tile * kTileKeys >= list) return;
+  float sum[kGroups][4] = {};
   // up to 32 query heads of the group at a time: their M and L, then their scores
+#pragma unroll 1
   for (int h1 = 0; h1 < g; h1 += 32) {
     const int count = min(32, g - h1);
     __syncthreads();
     if (threadIdx.x == 0) s_flag = 0;
     __syncthreads();
+#pragma unroll 1
     for (int h = warp; h < count; h += kJoinWarps) {
       const int hh = first + h1 + h;
       const int unit = (b * p.hg + hh / p.hpt) * p.mtiles + hh % p.hpt / kTileM, row = hh % p.hpt % kTileM;
@@ -728,10 +737,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 1) join_step_kernel(const Par
         L = (M == -INFINITY ? L : L * ex2(M - m)) + (ml.x == -INFINITY ? ml.y : ml.y * ex2(ml.x - m));
         M = m;
       }
-      const float mine_m = M;
+      const float mine = M;
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-      if (mine_m != -INFINITY) L *= ex2(mine_m - M);
+      if (mine != -INFINITY) L *= ex2(mine - M);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
       flag = __reduce_or_sync(0xffffffffu, flag);
@@ -742,42 +751,47 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 1) join_step_kernel(const Par
       }
     }
     __syncthreads();
-    if (mine) {
-      for (int h = 0; h < count; ++h) {
-        const int hh = first + h1 + h;
-        int k = k0;
+#pragma unroll 1
+    for (int h = 0; h < count; ++h) {
+      const int hh = first + h1 + h;
+      // a refused row and a row without any weight add nothing
+      const float l = s_l[h], neg = s_m[h], inv = 1.f / l;
+      const bool adds = !(s_flag >> h & 1) && l != 0.f;
+      const float* const sc = p.scores + size_t(b * p.H + hh) * p.score_stride;
+      const size_t at = size_t((b * p.H + hh) % p.L) * p.nb + t / BLK;
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) {
+        if (u[i] > t) continue;
+        int k = tile * kTileKeys + i * kGroupKeys + int(threadIdx.x) * 4;
         if (p.L > 1 && hh != h0) {
-          const int e = find_block(p, size_t((b * p.H + hh) % p.L) * p.nb + t / BLK, j);
+          const int e = find_block(p, at, u[i] / BLK);
           if (e < 0) continue;
           if (hh < h0) {                 // an earlier head of the group keeps the block and sums it
-            mine = false;
-            break;
+            u[i] = INT32_MAX;
+            continue;
           }
-          k = e * BLK + k0 % BLK;
+          k = e * BLK + u[i] % BLK;
         }
-        // a refused row and a row without any weight add nothing
-        const float l = s_l[h];
-        if ((s_flag >> h & 1) || l == 0.f) continue;
-        const float4 sc = *reinterpret_cast<const float4*>(p.scores + size_t(b * p.H + hh) * p.score_stride + k);
-        const float neg = s_m[h], inv = 1.f / l;
-        sum[0] = fmaf(ex2(fmaf(sc.x, p.scale_log2, neg)), inv, sum[0]);
-        sum[1] = fmaf(ex2(fmaf(sc.y, p.scale_log2, neg)), inv, sum[1]);
-        sum[2] = fmaf(ex2(fmaf(sc.z, p.scale_log2, neg)), inv, sum[2]);
-        sum[3] = fmaf(ex2(fmaf(sc.w, p.scale_log2, neg)), inv, sum[3]);
+        if (!adds) continue;
+        const float4 v = *reinterpret_cast<const float4*>(sc + k);
+        sum[i][0] = fmaf(ex2(fmaf(v.x, p.scale_log2, neg)), inv, sum[i][0]);
+        sum[i][1] = fmaf(ex2(fmaf(v.y, p.scale_log2, neg)), inv, sum[i][1]);
+        sum[i][2] = fmaf(ex2(fmaf(v.z, p.scale_log2, neg)), inv, sum[i][2]);
+        sum[i][3] = fmaf(ex2(fmaf(v.w, p.scale_log2, neg)), inv, sum[i][3]);
       }
     }
   }
-  if (mine) {
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (u + e <= t) to[e] = old[e] + sum[e];
-  }
+      if (u[i] <= t && u[i] + e <= t) w[u[i] + e] = old[i][e] + sum[i][e];
 }
 
 // The tree: one row (query head, drafted token) per warp, its runs joined with
 // its ancestors' keys.
 template <int BLK, int HD>
-__global__ void __launch_bounds__(kJoinWarps * 32, 3) join_tree_kernel(const Params p) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) join_tree_kernel(const Params p) {
   constexpr int DPL = HD / 32, CPL = HD / 8;
   __shared__ int s_par[kMaxT];
   __shared__ int s_path[kJoinWarps][kMaxT];       // ancestors from the token up to its root

@@ -20,10 +20,12 @@
 // order that the layout alone fixes.  Key/value heads whose kept blocks need
 // more than kStripBytes together are worked off in turns that share the workspace.
 //
-// Roles (448 threads, one CTA per SM): warp 0 looks items up and issues the TMA
-// loads, warp 1 the products; warps 2-13 take the sums in three groups, each a
-// tile of its own with a thread per key, so that on every scheduler one group
-// waits, loads and stores while the others' exponentials run.  (Sixteen warps
+// Roles (480 threads, one CTA per SM): warp 0 looks items up and loads their
+// query rows, warp 2 their keys (one warp for both issued a tile per 1300
+// cycles, with the products and sums waiting for it), warp 1 issues the
+// products; warps 3-14 take the sums in three groups, each a tile of its own
+// with a thread per key, so that on every scheduler one group waits, loads and
+// stores while the others' exponentials run.  (Sixteen warps
 // on one tile, four threads a key, met at a barrier per tile and left the
 // exponential unit idle in between: 175 us for the 32K dyadic route.)  Every
 // wait is bounded as in the forward.
@@ -47,13 +49,14 @@ namespace wts {
 using namespace ptx;
 
 constexpr int kGroups = 3;           // groups of four key warps, a tile each
-constexpr int kThreads = 64 + 128 * kGroups;
+constexpr int kThreads = 96 + 128 * kGroups;
 constexpr int kTileM = 128;          // keys of a tile
 constexpr int kQSlots = 2, kKSlots = 4;
 constexpr int kSBufs = 4;            // S buffers, one more than groups: the next product is ready in time
 // A group that is still at tile t lets the products get to t + 3, and the
 // producer is two items ahead of them: at most seven items are in use at once.
 constexpr int kItems = 8;
+static_assert(kKSlots == kSBufs, "a finished product releases its K slot and fills its S buffer");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint64_t kWaitNs = 1000000000ull, kDrainNs = 200000000ull;
 constexpr size_t kStripBytes = size_t(64) << 20;
@@ -86,10 +89,11 @@ struct Shape {
   static constexpr int kAtomQ = kNQ * 128, kAtomK = kTileM * 128;
   static constexpr int kOffK = kQSlots * kQBytes;
   static constexpr int kOffNeg = kOffK + kKSlots * kKBytes;   // [kItems][128] -lse log2 e
-  static constexpr int kOffItem = kOffNeg + kItems * 128 * 4;
+  static constexpr int kOffCols = kOffNeg + kItems * 128 * 4; // [kItems][32] the row's first key blocks
+  static constexpr int kOffItem = kOffCols + kItems * 32 * 4;
   static constexpr int kOffBar = kOffItem + kItems * 32;
-  // q_full, q_free, k_full, k_free, s_full, s_free, item, drain
-  static constexpr int kNumBars = 2 * kQSlots + 2 * kKSlots + 2 * kSBufs + kItems + 1;
+  // q_full, q_free, k_full, s_full, s_free, item, drain
+  static constexpr int kNumBars = 2 * kQSlots + kKSlots + 2 * kSBufs + kItems + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kUsed = kOffMisc + 16;
   // more than half of an SM's shared memory, so that no second CTA shares it:
@@ -101,13 +105,13 @@ struct Shape {
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
-// A work item as the producer announces it; tiles 0 ends the stream.
+// A work item as the first warp announces it; tiles 0 ends the stream.
 struct Item {
   int tiles, blocks;         // tiles and kept blocks of the row
   int diag;                  // the last kept block is the diagonal one
   int dead;                  // a query row of the item has lse = -inf
   int64_t slot;              // first row of partial sums
-  int64_t pad;
+  int e0, kv;                // first entry in col_idx; key/value head
 };
 static_assert(sizeof(Item) == 32, "item ring");
 
@@ -125,6 +129,13 @@ __device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
       : "+f"(d0), "+f"(d1)
       : "f"(a0), "f"(a1));
 }
+// True in one thread of the warp, which is the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Waits for the loads of TMEM into v; the registers are operands so that no
 // use of them is moved before it while other loads are in flight.
 __device__ __forceinline__ void wait_ld32(float* v) {
@@ -152,9 +163,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t sQ = base, sK = base + S::kOffK, bar0 = base + S::kOffBar;
   const uint32_t bQFull0 = bar0, bQFree0 = bQFull0 + 8u * kQSlots, bKFull0 = bQFree0 + 8u * kQSlots,
-                 bKFree0 = bKFull0 + 8u * kKSlots, bSFull0 = bKFree0 + 8u * kKSlots, bSFree0 = bSFull0 + 8u * kSBufs,
-                 bItem0 = bSFree0 + 8u * kSBufs, bDrain = bItem0 + 8u * kItems;
+                 bSFull0 = bKFull0 + 8u * kKSlots, bSFree0 = bSFull0 + 8u * kSBufs, bItem0 = bSFree0 + 8u * kSBufs,
+                 bDrain = bItem0 + 8u * kItems;
   float* negs = reinterpret_cast<float*>(smem + S::kOffNeg);
+  volatile int* colss = reinterpret_cast<volatile int*>(smem + S::kOffCols);
   volatile Item* ring = reinterpret_cast<volatile Item*>(smem + S::kOffItem);
   volatile uint32_t* tmem_holder = reinterpret_cast<volatile uint32_t*>(smem + S::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kOffMisc + 4);
@@ -165,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return ctl.wait(first + 8u * (x % depth), uint32_t(x / depth) & 1u);
   };
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2 * kQSlots + 2 * kKSlots + kSBufs; ++s) mbar_init(bQFull0 + 8u * s, 1);
+    for (int s = 0; s < 2 * kQSlots + kKSlots + kSBufs; ++s) mbar_init(bQFull0 + 8u * s, 1);
     for (int s = 0; s < kSBufs; ++s) mbar_init(bSFree0 + 8u * s, 4);
     for (int s = 0; s < kItems; ++s) mbar_init(bItem0 + 8u * s, 1);
     mbar_init(bDrain, 1);
@@ -186,12 +198,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Items with kept blocks are counted by k, their tiles over all of them by t:
   // item k uses Q slot k % 2 and ring entry k % 8, tile t K slot and S buffer t % 4.
   if (warp == 0) {
-    // ================================================================ loads
+    // ================================================================ items and query rows
     // An item is looked up in two steps, its row's place in the layout and then
     // its key blocks and lse, each of them an item's time ahead of its use: done
     // one after the other when the item comes up they take 4 us, which is the
     // time of four tiles.
-    int k = 0, t = 0;
+    const bool leader = elect_one();
+    int k = 0;
     bool ok = true;
     struct Row {
       int unit, i, f0, e0, len;          // e0, len: still in flight until the next step
@@ -229,12 +242,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return w;
     };
-    uint32_t it = blockIdx.x;
-    Row cur = find_row(it), next = find_row(it + gridDim.x);
+    // rounds of one item per CTA, every other one the other way round, so that
+    // no CTA has the longer row of each
+    auto item = [&](uint32_t round) -> uint32_t {
+      return round * gridDim.x + (round & 1u ? gridDim.x - 1u - blockIdx.x : blockIdx.x);
+    };
+    const uint32_t rounds = (p.items + gridDim.x - 1) / gridDim.x;
+    Row cur = find_row(item(0)), next = find_row(item(1));
     Found mine = find_keys(cur);
-    while (cur.len >= 0 && ok) {
-      it += gridDim.x;
-      const Row after = find_row(it + gridDim.x);
+    for (uint32_t round = 0; round < rounds && ok; ++round) {
+      const Row after = find_row(item(round + 2));
       const Found theirs = find_keys(next);
       const int e0 = cur.e0, len = cur.len - cur.e0, i = cur.i;
       const Found w = mine;
@@ -253,54 +270,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       dead = __any_sync(0xffffffffu, dead);
       if (k >= kQSlots && !(ok = __all_sync(0xffffffffu, wait(bQFree0, kQSlots, k - kQSlots)))) break;
-      const int tiles = (len + S::kBPT - 1) / S::kBPT;
 #pragma unroll
       for (int x = 0; x < NQ32; ++x) negs[(k % kItems) * 128 + x * 32 + lane] = neg[x];
+      colss[(k % kItems) * 32 + lane] = w.cols;
       __syncwarp();
-      if (lane == 0) {
+      const uint32_t bq = bQFull0 + 8u * (k % kQSlots), dst = sQ + (k % kQSlots) * S::kQBytes;
+      if (leader) {
         volatile Item* e = ring + k % kItems;
-        e->tiles = tiles;
+        e->tiles = (len + S::kBPT - 1) / S::kBPT;
         e->blocks = len;
         e->diag = w.last == i;
         e->dead = dead;
         e->slot = int64_t(row.unit) * p.slots + (e0 - w.base);
+        e->e0 = e0;
+        e->kv = row.f0 / p.g;
         mbar_arrive(bItem0 + 8u * (k % kItems));
-        const uint32_t bq = bQFull0 + 8u * (k % kQSlots), dst = sQ + (k % kQSlots) * S::kQBytes;
         mbar_expect_tx(bq, S::kQBytes);
-#pragma unroll
-        for (int h = 0; h < PACK; ++h)
-#pragma unroll
-          for (int a = 0; a < HD / 64; ++a)
-            tma_load_3d(dst + a * S::kAtomQ + h * BLK * 128, &tmQ, bq, a * 64, i * BLK, row.f0 + h);
+        // one box: the block of one head, or of two heads stacked
+        if constexpr (BLK == 64 && PACK == 1) tma_load_kv<HD>(dst, &tmQ, bq, i * BLK, row.f0);
+        else tma_load_q<BLK, HD>(dst, &tmQ, bq, i * BLK, row.f0);
       }
+      __syncwarp();
       ++k;
-      const int kv = row.f0 / p.g;
-      int have = 0, cols = w.cols;       // lane x holds entry have + x
-      for (int y = 0; y < tiles; ++y) {
-        if (y * S::kBPT - have >= 32) {
-          have = y * S::kBPT;
-          cols = have + lane < len ? p.col_idx[e0 + have + lane] : 0;
-        }
-        if (t >= kKSlots && !(ok = __all_sync(0xffffffffu, wait(bKFree0, kKSlots, t - kKSlots)))) break;
-        // a last tile without a second block leaves that half as it was: its sums are not stored
-        const int blocks = min(S::kBPT, len - y * S::kBPT);
-        const uint32_t bk = bKFull0 + 8u * (t % kKSlots), dst = sK + (t % kKSlots) * S::kKBytes;
-        if (lane == 0) mbar_expect_tx(bk, uint32_t(blocks) * (S::kKBytes / S::kBPT));
-#pragma unroll
-        for (int x = 0; x < S::kBPT; ++x) {
-          const int j = __shfl_sync(0xffffffffu, cols, (y * S::kBPT + x - have) & 31);
-          if (lane == 0 && x < blocks) {
-#pragma unroll
-            for (int a = 0; a < HD / 64; ++a)
-              tma_load_3d(dst + a * S::kAtomK + x * BLK * 128, &tmK, bk, a * 64, j * BLK, kv);
-          }
-        }
-        ++t;
-      }
     }
     // the end of the stream, in an entry that the sums are done with
     if (ok && k >= kQSlots) ok = __all_sync(0xffffffffu, wait(bQFree0, kQSlots, k - kQSlots));
-    if (lane == 0) {
+    if (leader) {
       if (ok) {
         ring[k % kItems].tiles = 0;
         mbar_arrive(bItem0 + 8u * (k % kItems));
@@ -308,47 +303,92 @@ __global__ void __launch_bounds__(kThreads, 1)
       // never leave the CTA with copies in flight into its shared memory
       for (int x = k > kQSlots ? k - kQSlots : 0; x < k; ++x)
         wait_drain(bQFull0 + 8u * (x % kQSlots), uint32_t(x / kQSlots) & 1u, kDrainNs);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ================================================================ keys
+    const bool leader = elect_one();
+    bool ok = true;
+    int t = 0;
+    for (int k = 0; ok; ++k) {
+      if (!(ok = __all_sync(0xffffffffu, wait(bItem0, kItems, k)))) break;
+      volatile Item* e = ring + k % kItems;
+      const int tiles = e->tiles;
+      if (tiles == 0) break;
+      const int len = e->blocks, e0 = e->e0, kv = e->kv;
+      int have = 0, cols = colss[(k % kItems) * 32 + lane];   // lane x holds entry have + x
+      for (int y = 0; y < tiles; ++y, ++t) {
+        if (y * S::kBPT - have >= 32) {
+          have = y * S::kBPT;
+          cols = have + lane < len ? p.col_idx[e0 + have + lane] : 0;
+        }
+        // the product that filled this tile's S buffer last has read its K slot
+        if (t >= kKSlots && !(ok = __all_sync(0xffffffffu, wait(bSFull0, kSBufs, t - kKSlots)))) break;
+        // a last tile without a second block leaves that half as it was: its sums are not stored
+        const int blocks = min(S::kBPT, len - y * S::kBPT);
+        const uint32_t bk = bKFull0 + 8u * (t % kKSlots), dst = sK + (t % kKSlots) * S::kKBytes;
+        const int j0 = __shfl_sync(0xffffffffu, cols, y * S::kBPT - have);
+        const int j1 = __shfl_sync(0xffffffffu, cols, (y * S::kBPT + S::kBPT - 1 - have) & 31);
+        if (leader) {
+          mbar_expect_tx(bk, uint32_t(blocks) * (S::kKBytes / S::kBPT));
+#pragma unroll
+          for (int a = 0; a < HD / 64; ++a) tma_load_3d(dst + a * S::kAtomK, &tmK, bk, a * 64, j0 * BLK, kv);
+          if (S::kBPT == 2 && blocks == 2) {
+#pragma unroll
+            for (int a = 0; a < HD / 64; ++a)
+              tma_load_3d(dst + a * S::kAtomK + BLK * 128, &tmK, bk, a * 64, j1 * BLK, kv);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    if (leader)
       for (int x = t > kKSlots ? t - kKSlots : 0; x < t; ++x)
         wait_drain(bKFull0 + 8u * (x % kKSlots), uint32_t(x / kKSlots) & 1u, kDrainNs);
-    }
+    __syncwarp();
   } else if (warp == 1) {
     // ================================================================ products
-    if (lane == 0) {
-      constexpr uint64_t kFix = sw128_fixed(16, 1024);
-      constexpr uint32_t kHi = uint32_t(kFix >> 32);
-      const uint32_t q_lo = uint32_t(kFix) + (sQ >> 4), k_lo = uint32_t(kFix) + (sK >> 4);
-      bool ok = true;
-      int t = 0;
-      for (int k = 0; ok; ++k) {
-        if (!(ok = wait(bItem0, kItems, k))) break;
-        const int tiles = ring[k % kItems].tiles;
-        if (tiles == 0) break;
-        if (!(ok = wait(bQFull0, kQSlots, k))) break;
-        const uint32_t qb = q_lo + uint32_t(k % kQSlots) * (S::kQBytes >> 4);
-        for (int y = 0; y < tiles; ++y) {
-          if (!(ok = wait(bKFull0, kKSlots, t))) break;
-          if (t >= kSBufs && !(ok = wait(bSFree0, kSBufs, t - kSBufs))) break;
-          tc_fence_after();
-          const uint32_t kb = k_lo + uint32_t(t % kKSlots) * (S::kKBytes >> 4);
-          const uint32_t d = tmem + (t % kSBufs) * S::kNQ;
+    // The whole warp goes through the loop, so that what a product is given
+    // stays in uniform registers; one elected thread issues.
+    constexpr uint64_t kFix = sw128_fixed(16, 1024);
+    constexpr uint32_t kHi = uint32_t(kFix >> 32);
+    const uint32_t q_lo = uint32_t(kFix) + (sQ >> 4), k_lo = uint32_t(kFix) + (sK >> 4);
+    const bool leader = elect_one();
+    bool ok = true;
+    int t = 0;
+    for (int k = 0; ok; ++k) {
+      if (!(ok = __all_sync(0xffffffffu, wait(bItem0, kItems, k)))) break;
+      const int tiles = ring[k % kItems].tiles;
+      if (tiles == 0) break;
+      if (!(ok = __all_sync(0xffffffffu, wait(bQFull0, kQSlots, k)))) break;
+      const uint32_t qb = q_lo + uint32_t(k % kQSlots) * (S::kQBytes >> 4);
+      for (int y = 0; y < tiles; ++y, ++t) {
+        ok = wait(bKFull0, kKSlots, t) && (t < kSBufs || wait(bSFree0, kSBufs, t - kSBufs));
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_after();
+        const uint32_t kb = k_lo + uint32_t(t % kKSlots) * (S::kKBytes >> 4);
+        const uint32_t d = tmem + (t % kSBufs) * S::kNQ;
+        if (leader) {
 #pragma unroll
           for (int kk = 0; kk < HD / 16; ++kk)
             mma_ss(d, desc_from(kb + ((kk >> 2) * S::kAtomK + (kk & 3) * 32) / 16, kHi),
                    desc_from(qb + ((kk >> 2) * S::kAtomQ + (kk & 3) * 32) / 16, kHi), S::kIdesc, kk > 0 ? 1u : 0u);
           tc_commit(bSFull0 + 8u * (t % kSBufs));
-          tc_commit(bKFree0 + 8u * (t % kKSlots));
           if (y == tiles - 1) tc_commit(bQFree0 + 8u * (k % kQSlots));
-          ++t;
         }
+        __syncwarp();
       }
+    }
+    if (leader) {
       tc_commit(bDrain);
       wait_drain(bDrain, 0, kDrainNs);
     }
+    __syncwarp();
   } else {
     // ================================================================ sums
     // Group t % 3 of four warps takes tile t, a key per thread; warp w reaches
     // TMEM lanes 32 (w % 4) .., so each scheduler has a warp of every group.
-    const int q4 = warp & 3, group = (warp - 2) >> 2;
+    const int q4 = warp & 3, group = (warp - 3) >> 2;
     const int key = q4 * 32 + lane;
     const int half = key / BLK, kl = key - half * BLK;         // key block of the tile, key in it
     const uint32_t lane_base = tmem + (uint32_t(q4 * 32) << 16);
@@ -423,44 +463,98 @@ __global__ void __launch_bounds__(kThreads, 1)
 // w[kv][u] += the sums of u's block, unit by unit and row by row.  A block of
 // 1024 threads takes the SL = 1024 / B key blocks j0 .. j0 + SL - 1, a slice of
 // B threads for each; a column of more than kLong rows (a global first block's)
-// is shared out over all slices.
-constexpr int kAddThreads = 1024, kLong = 64;
+// is shared out over the whole block, four keys a thread.  What this costs is
+// the latency of its loads, so those of the layout are made before the wait for
+// the first kernel, and those of the sums many at a time.
+constexpr int kAddThreads = 1024, kLong = 32, kStaged = 4096, kUnits = 8;
 template <int BLK>
 __global__ void __launch_bounds__(kAddThreads) add_rows_kernel(const Params p) {
-  constexpr int SL = kAddThreads / BLK;
-  __shared__ int s_col[SL + 1];
-  __shared__ float s_sum[kAddThreads];
+  constexpr int SL = kAddThreads / BLK, RL = kAddThreads / (BLK / 4);
+  __shared__ int s_col[kUnits][SL + 1];          // where the block's columns begin, for each unit
+  __shared__ int s_pos[kStaged];                 // csr_pos of the block's columns, if they fit
+  __shared__ float4 s_sum[kAddThreads];
   const int per = (p.nb + SL - 1) / SL;
   const int kvl = blockIdx.x / per, j0 = (blockIdx.x - kvl * per) * SL;
   const int sl = threadIdx.x / BLK, kl = threadIdx.x % BLK;
   const int u = (j0 + sl) * BLK + kl;
   float sum = 0.f;
-  asm volatile("griddepcontrol.wait;" ::: "memory");     // the sums are in memory from here on
-  for (int x0 = 0; x0 < p.upk; ++x0) {
-    const int unit = kvl * p.upk + x0;
-    const int lh = (p.kv0 * p.upk + unit) * p.pack % p.L;
-    const size_t h0 = size_t(lh) * p.nb;
-    const float* const src = p.part + (int64_t(unit) * p.slots - p.row_ptr[h0]) * BLK + kl;
+#pragma unroll 1
+  for (int x0 = 0; x0 < p.upk; x0 += kUnits) {
+    const int units = min(kUnits, p.upk - x0);
     __syncthreads();
-    if (threadIdx.x <= SL) s_col[threadIdx.x] = p.col_ptr[h0 + min(j0 + int(threadIdx.x), p.nb)];
+    for (int x = threadIdx.x; x < units * (SL + 1); x += kAddThreads) {
+      const int lh = (p.kv0 * p.upk + kvl * p.upk + x0 + x / (SL + 1)) * p.pack % p.L;
+      s_col[x / (SL + 1)][x % (SL + 1)] = p.col_ptr[size_t(lh) * p.nb + min(j0 + x % (SL + 1), p.nb)];
+    }
     __syncthreads();
-    // the sums of entries c, c + step, .. below c1, in this order
-    auto add = [&](int c, int c1, int step) {
-      float t = 0.f;
-#pragma unroll 8
-      for (; c < c1; c += step) t += src[int64_t(p.csr_pos[c]) * BLK];
-      return t;
-    };
-    const int c0 = s_col[sl], c1 = s_col[sl + 1];
-    if (c1 - c0 <= kLong) sum += add(c0, c1, 1);
-    for (int x = 0; x < SL; ++x) {
-      const int d0 = s_col[x], d1 = s_col[x + 1];
-      if (d1 - d0 <= kLong) continue;
-      __syncthreads();
-      s_sum[threadIdx.x] = add(d0 + sl, d1, SL);
-      __syncthreads();
-      if (sl == x)
-        for (int y = 0; y < SL; ++y) sum += s_sum[y * BLK + kl];
+    int total = 0;
+    for (int x = 0; x < units; ++x) total += s_col[x][SL] - s_col[x][0];
+    const bool staged = total <= kStaged;
+    if (staged) {
+      int off = 0;
+      for (int x = 0; x < units; ++x) {
+        const int e0 = s_col[x][0], n = s_col[x][SL] - e0;
+        for (int y = threadIdx.x; y < n; y += kAddThreads) s_pos[off + y] = p.csr_pos[e0 + y];
+        off += n;
+      }
+    }
+    __syncthreads();
+    if (x0 == 0) asm volatile("griddepcontrol.wait;" ::: "memory");   // the sums are in memory from here on
+    int off = 0;
+#pragma unroll 1
+    for (int x = 0; x < units; ++x) {
+      const int unit = kvl * p.upk + x0 + x;
+      const int lh = (p.kv0 * p.upk + unit) * p.pack % p.L;
+      const float* const src = p.part + (int64_t(unit) * p.slots - p.row_ptr[size_t(lh) * p.nb]) * BLK;
+      const int shift = off - s_col[x][0];       // entry c is s_pos[c + shift]
+      off += s_col[x][SL] - s_col[x][0];
+      auto pos = [&](int c) -> int64_t { return staged ? s_pos[c + shift] : p.csr_pos[c]; };
+      const int c0 = s_col[x][sl], c1 = s_col[x][sl + 1];
+      const bool mine = c1 - c0 <= kLong;
+      if (mine) {
+#pragma unroll 1
+        for (int c = c0; c < c1; c += 8) {
+          float v[8];
+#pragma unroll
+          for (int y = 0; y < 8; ++y) v[y] = src[pos(min(c + y, c1 - 1)) * BLK + kl];
+#pragma unroll
+          for (int y = 0; y < 8; ++y) sum += c + y < c1 ? v[y] : 0.f;
+        }
+      }
+      if (__syncthreads_and(mine)) continue;
+#pragma unroll 1
+      for (int y = 0; y < SL; ++y) {
+        const int d0 = s_col[x][y], d1 = s_col[x][y + 1];
+        if (d1 - d0 <= kLong) continue;
+        const int rl = threadIdx.x / (BLK / 4), k4 = threadIdx.x % (BLK / 4);
+        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int c = d0 + rl; c < d1; c += 4 * RL) {
+          float4 v[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            v[z] = reinterpret_cast<const float4*>(src + pos(min(c + z * RL, d1 - 1)) * BLK)[k4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            if (c + z * RL >= d1) break;
+            t.x += v[z].x;
+            t.y += v[z].y;
+            t.z += v[z].z;
+            t.w += v[z].w;
+          }
+        }
+        __syncthreads();
+        s_sum[threadIdx.x] = t;                  // [RL][BLK] floats
+        __syncthreads();
+        float* const f = reinterpret_cast<float*>(s_sum);
+        float part = 0.f;
+        for (int z = sl; z < RL; z += SL) part += f[z * BLK + kl];
+        __syncthreads();
+        f[threadIdx.x] = part;
+        __syncthreads();
+        if (sl == y)
+          for (int z = 0; z < SL; ++z) sum += f[z * BLK + kl];
+      }
     }
   }
   // a wait that ran out left sums unwritten: nothing is added then
@@ -511,7 +605,7 @@ int launch(const void* q, const void* k, int kv_heads, Params p, const bsa_layou
     n_sm = sms[dev];
   }
   CUtensorMap mq, mk;
-  int st = tmap::encode_atoms(&mq, q, p.heads, p.n, HD, BLK);
+  int st = BLK == 64 && PACK == 1 ? tmap::encode_kv(&mq, q, p.heads, p.n, HD) : tmap::encode_q(&mq, q, p.heads, p.n, HD, BLK);
   if (st == BSA_OK) st = tmap::encode_atoms(&mk, k, kv_heads, p.n, HD, BLK);
   if (st != BSA_OK) return st;
   const int strip = strip_of(layout, p.heads, kv_heads);
