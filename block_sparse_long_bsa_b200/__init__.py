@@ -438,11 +438,11 @@ def bsa_decode_tree(q, k_tree, v_tree, k_cache, v_cache, page_table, max_blocks:
                                _stream(stream)))
 
 
-def _want(device: int, dtype, checks) -> None:
+def _want(device: int, dtype, *checks) -> None:
     """Each (name, tensor, shape) contiguous, of the dtype and shape, on the
-    device; None is skipped."""
+    device."""
     for name, t, shape in checks:
-        if t is None or (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device):
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device:
             continue
         what = str(dtype).replace("torch.", "")
         if t.dtype is not dtype or not t.is_contiguous():
@@ -452,14 +452,15 @@ def _want(device: int, dtype, checks) -> None:
         raise BsaError(2, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
 
 
-def _rows_of(layout: "Layout", rows: int, checks) -> int:
+def _rows_of(layout: "Layout", rows: int, *checks) -> int:
     """The common distance between the rows of arrays [rows, >= n] whose last
     dimension is contiguous; ``checks`` of (name, tensor, dtype), None skipped."""
     n, stride = layout.n, None
     for name, t, dtype in checks:
         if t is None:
             continue
-        if t.dtype is not dtype or t.dim() != 2 or t.shape[0] != rows or t.shape[1] < n or t.stride(1) != 1:
+        shape = t.shape
+        if t.dtype is not dtype or len(shape) != 2 or shape[0] != rows or shape[1] < n or t.stride(1) != 1:
             raise BsaError(2, f"{name} must be a {str(dtype).replace('torch.', '')} tensor of {rows} rows of at least "
                               f"{n}, contiguous along them")
         if t.get_device() != layout.device:
@@ -485,16 +486,17 @@ def _on(stream):
     return torch.cuda.stream(stream)
 
 
-def _workspace(layout: "Layout", need, workspace, stream):
-    """The given workspace, or a new one of ``need()`` bytes that torch holds
-    for ``stream``; (tensor, bytes)."""
-    import torch
+def _workspace(layout: "Layout", workspace, stream, bytes_of, *sizes):
+    """The given workspace, or a new one of ``bytes_of(handle, *sizes)`` bytes
+    that torch holds for ``stream``; (tensor, bytes)."""
     if workspace is None:
+        import torch
         with _on(stream):
-            workspace = torch.empty(max(need(), 16), dtype=torch.uint8, device=f"cuda:{layout.device}")
+            workspace = torch.empty(max(bytes_of(layout.handle, *sizes), 16), dtype=torch.uint8,
+                                    device=f"cuda:{layout.device}")
     elif not workspace.is_contiguous() or workspace.get_device() != layout.device:
         raise BsaError(1, f"workspace must be a contiguous tensor on cuda:{layout.device}")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace, workspace.nbytes
 
 
 def attention_weights(q, k, lse, layout: "Layout", weights=None, scale: float | None = None, workspace=None,
@@ -508,15 +510,16 @@ def attention_weights(q, k, lse, layout: "Layout", weights=None, scale: float | 
     dev, h = layout.device, layout.handle
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    _want(dev, torch.bfloat16, (("q", q, (heads, layout.n, d)), ("k", k, (kv_heads, layout.n, d))))
-    _want(dev, torch.float32, (("lse", lse, (heads, layout.n)),))
+    _want(dev, torch.bfloat16, ("q", q, (heads, layout.n, d)), ("k", k, (kv_heads, layout.n, d)))
+    _want(dev, torch.float32, ("lse", lse, (heads, layout.n)))
     if weights is None:
         with _on(stream):
             weights = torch.zeros((kv_heads, n), dtype=torch.float32, device=q.device)
-    stride = _rows_of(layout, kv_heads, (("weights", weights, torch.float32),))
-    workspace, size = _workspace(layout, lambda: bsa_attention_weights_workspace_bytes(h, heads, kv_heads), workspace,
-                                 stream)
-    bsa_attention_weights(q, k, lse, h, layout.B, n, heads, kv_heads, d, scale, weights, stride, workspace, size, stream)
+    stride = _rows_of(layout, kv_heads, ("weights", weights, torch.float32))
+    workspace, size = _workspace(layout, workspace, stream, bsa_attention_weights_workspace_bytes, heads, kv_heads)
+    _check(load_library().bsa_attention_weights(
+        q.data_ptr(), k.data_ptr(), lse.data_ptr(), h, layout.B, n, heads, kv_heads, d, scale, weights.data_ptr(),
+        stride, workspace.data_ptr(), size, _stream(stream)))
     return weights
 
 
@@ -536,15 +539,17 @@ def decode_weights(q, k_cache, v_cache, page_table, positions, layout: "Layout",
             o = torch.empty_like(q) if o is None else o
             lse = torch.empty((heads,), dtype=torch.float32, device=q.device) if lse is None else lse
     cache = (pages, hkv, layout.B, d)
-    _want(dev, torch.bfloat16, (("q", q, (heads, d)), ("k_cache", k_cache, cache), ("v_cache", v_cache, cache),
-                                ("o", o, (heads, d))))
-    _want(dev, torch.int32, (("page_table", page_table, (batch, max_blocks)), ("positions", positions, (batch,))))
-    _want(dev, torch.float32, (("lse", lse, (heads,)),))
-    stride = _rows_of(layout, batch * hkv, (("weights", weights, torch.float32),))
-    workspace, size = _workspace(
-        layout, lambda: bsa_decode_weights_workspace_bytes(h, batch, heads, batch * hkv, d), workspace, stream)
-    bsa_decode_weights(q, k_cache, v_cache, page_table, max_blocks, pages, positions, h, batch, heads, batch * hkv, d,
-                       scale, o, lse, weights, stride, workspace, size, stream)
+    _want(dev, torch.bfloat16, ("q", q, (heads, d)), ("k_cache", k_cache, cache), ("v_cache", v_cache, cache),
+          ("o", o, (heads, d)))
+    _want(dev, torch.int32, ("page_table", page_table, (batch, max_blocks)), ("positions", positions, (batch,)))
+    _want(dev, torch.float32, ("lse", lse, (heads,)))
+    stride = _rows_of(layout, batch * hkv, ("weights", weights, torch.float32))
+    workspace, size = _workspace(layout, workspace, stream, bsa_decode_weights_workspace_bytes, batch, heads,
+                                 batch * hkv, d)
+    _check(load_library().bsa_decode_weights(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), max_blocks, pages,
+        positions.data_ptr(), h, batch, heads, batch * hkv, d, scale, o.data_ptr(), lse.data_ptr(), weights.data_ptr(),
+        stride, workspace.data_ptr(), size, _stream(stream)))
     return o, lse
 
 
@@ -569,15 +574,17 @@ def evict(k_cache, v_cache, page_table, lengths, weights, layout: "Layout", budg
             tokens_out = like(torch.int32) if tokens_out is None else tokens_out
             lengths_out = torch.empty_like(lengths) if lengths_out is None else lengths_out
     cache = (pages, hkv, layout.B, d)
-    _want(dev, torch.bfloat16, (("k_cache", k_cache, cache), ("v_cache", v_cache, cache)))
-    _want(dev, torch.int32, (("page_table", page_table, (batch, max_blocks)), ("lengths", lengths, (batch,)),
-                             ("lengths_out", lengths_out, (batch,))))
-    stride = _rows_of(layout, rows, (("weights", weights, torch.float32), ("tokens", tokens, torch.int32),
-                                     ("weights_out", weights_out, torch.float32),
-                                     ("tokens_out", tokens_out, torch.int32)))
-    workspace, size = _workspace(layout, lambda: bsa_evict_workspace_bytes(h, batch, rows, budget), workspace, stream)
-    bsa_evict(k_cache, v_cache, page_table, max_blocks, pages, lengths, weights, tokens, h, batch, rows, d, budget,
-              recent, stride, weights_out, tokens_out, lengths_out, workspace, size, stream)
+    _want(dev, torch.bfloat16, ("k_cache", k_cache, cache), ("v_cache", v_cache, cache))
+    _want(dev, torch.int32, ("page_table", page_table, (batch, max_blocks)), ("lengths", lengths, (batch,)),
+          ("lengths_out", lengths_out, (batch,)))
+    stride = _rows_of(layout, rows, ("weights", weights, torch.float32), ("tokens", tokens, torch.int32),
+                      ("weights_out", weights_out, torch.float32), ("tokens_out", tokens_out, torch.int32))
+    workspace, size = _workspace(layout, workspace, stream, bsa_evict_workspace_bytes, batch, rows, budget)
+    _check(load_library().bsa_evict(
+        k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), max_blocks, pages, lengths.data_ptr(),
+        weights.data_ptr(), 0 if tokens is None else tokens.data_ptr(), h, batch, rows, d, budget, recent, stride,
+        weights_out.data_ptr(), tokens_out.data_ptr(), lengths_out.data_ptr(), workspace.data_ptr(), size,
+        _stream(stream)))
     return weights_out, tokens_out, lengths_out
 
 
@@ -599,15 +606,17 @@ def decode_tree(q, k_tree, v_tree, k_cache, v_cache, page_table, lengths, parent
             o = torch.empty_like(q) if o is None else o
             lse = torch.empty((heads, T), dtype=torch.float32, device=q.device) if lse is None else lse
     rows, tree, cache = (heads, T, d), (batch * hkv, T, d), (pages, hkv, layout.B, d)
-    _want(dev, torch.bfloat16, (("q", q, rows), ("k_tree", k_tree, tree), ("v_tree", v_tree, tree),
-                                ("k_cache", k_cache, cache), ("v_cache", v_cache, cache), ("o", o, rows)))
-    _want(dev, torch.int32, (("page_table", page_table, (batch, max_blocks)), ("lengths", lengths, (batch,)),
-                             ("parents", parents, (batch, T))))
-    _want(dev, torch.float32, (("lse", lse, (heads, T)),))
-    workspace, size = _workspace(
-        layout, lambda: bsa_decode_tree_workspace_bytes(h, batch, heads, batch * hkv, T, d), workspace, stream)
-    bsa_decode_tree(q, k_tree, v_tree, k_cache, v_cache, page_table, max_blocks, pages, lengths, parents, h, T, batch,
-                    heads, batch * hkv, d, scale, o, lse, workspace, size, stream)
+    _want(dev, torch.bfloat16, ("q", q, rows), ("k_tree", k_tree, tree), ("v_tree", v_tree, tree),
+          ("k_cache", k_cache, cache), ("v_cache", v_cache, cache), ("o", o, rows))
+    _want(dev, torch.int32, ("page_table", page_table, (batch, max_blocks)), ("lengths", lengths, (batch,)),
+          ("parents", parents, (batch, T)))
+    _want(dev, torch.float32, ("lse", lse, (heads, T)))
+    workspace, size = _workspace(layout, workspace, stream, bsa_decode_tree_workspace_bytes, batch, heads, batch * hkv,
+                                 T, d)
+    _check(load_library().bsa_decode_tree(
+        q.data_ptr(), k_tree.data_ptr(), v_tree.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        page_table.data_ptr(), max_blocks, pages, lengths.data_ptr(), parents.data_ptr(), h, T, batch, heads,
+        batch * hkv, d, scale, o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), size, _stream(stream)))
     return o, lse
 
 

@@ -101,6 +101,12 @@ static __device__ __noinline__ void wait_drain(uint32_t bar, uint32_t parity, ui
 __device__ __forceinline__ void fence_barrier_init() {
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
+// Programmatic dependent launch: a kernel launched with the attribute may
+// start while the one before it in the stream still runs; grid_wait returns
+// once that one has ended with its writes visible, grid_release lets the next
+// one start as soon as every block of this one has got here.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 // TMA (no multicast anywhere in this library).
 __device__ __forceinline__ void tma_prefetch(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");

@@ -26,10 +26,14 @@
 #include <mutex>
 #include <string>
 
+#include "bsa_device.cuh"
 #include "bsa_internal.h"
 
 namespace bsa {
 namespace evict {
+
+using ptx::grid_release;
+using ptx::grid_wait;
 
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 4 * kSelThreads;          // of an 11-bit digit, four a thread
@@ -56,9 +60,6 @@ struct Params {
   size_t stride;              // of weights, tokens and their outputs
   int n, B, max_blocks, num_pages, hkv, budget, recent, cap;
 };
-
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Order-preserving key of a weight; a NaN counts as -inf, -0 as 0.
 __device__ __forceinline__ uint32_t key_of(float w) {
@@ -107,10 +108,14 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
   __shared__ __align__(16) int sums[3][kBins];    // the cluster's, a digit each
   __shared__ int s_scan[3][kSelWarps];
   __shared__ int s_bad, s_newest, s_digit, s_left, s_equal, s_holes, s_movers;
-  grid_release();
   const int row = blockIdx.x / C, rank = cluster_rank();
   const int b = row / p.hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  reinterpret_cast<int4*>(hist)[tid] = make_int4(0, 0, 0, 0);
+#pragma unroll
+  for (int d = 0; d < 3; ++d) reinterpret_cast<int4*>(sums[d])[tid] = make_int4(0, 0, 0, 0);
+  grid_wait();                                   // nothing of the caller's is read or written before this
+  grid_release();
   const int len = p.lengths[b];
   const float* w = p.weights + size_t(row) * p.stride;
   const int32_t* tok = p.tokens ? p.tokens + size_t(row) * p.stride : nullptr;
@@ -128,9 +133,6 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
     }
     if (bad) s_bad = 1;
   }
-  reinterpret_cast<int4*>(hist)[tid] = make_int4(0, 0, 0, 0);
-#pragma unroll
-  for (int d = 0; d < 3; ++d) reinterpret_cast<int4*>(sums[d])[tid] = make_int4(0, 0, 0, 0);
   __syncthreads();
   if (s_bad) {
     if (tid == 0 && rank == 0) {
@@ -333,6 +335,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const Params p, int 
   const int b = row / p.hkv, hk = row - b * p.hkv;
   const int lane = threadIdx.x & 31;
   const int s = tile * kMoveThreads + threadIdx.x;
+  // (no early start for the kernel after this one: the next cut's blocks took
+  // room from the moves, 47 us a call against 49)
   grid_wait();
   const int4 m = p.meta[row];
   if (m.z) {                             // refused: left as it was
@@ -431,33 +435,13 @@ int launch(const Params& p, int rows, int d, cudaStream_t stream) {
   int C = 1;
   while (C < kMaxCluster && p.n > C * kSlotsPerBlock && rows * C <= 148) C *= 2;
   const int per = (p.n + C * 32 - 1) / (C * 32) * 32;
-  cudaLaunchConfig_t sel = {};
-  sel.gridDim = dim3(unsigned(rows) * unsigned(C), 1, 1);
-  sel.blockDim = dim3(kSelThreads, 1, 1);
-  sel.dynamicSmemBytes = size_t(std::min(per, kKeysInSmem)) * 4;
-  sel.stream = stream;
-  cudaLaunchAttribute cl[1];
-  cl[0].id = cudaLaunchAttributeClusterDimension;
-  cl[0].val.clusterDim.x = unsigned(C);
-  cl[0].val.clusterDim.y = 1;
-  cl[0].val.clusterDim.z = 1;
-  sel.attrs = cl;
-  sel.numAttrs = 1;
-  e = cudaLaunchKernelEx(&sel, select_kernel, p, C);
-  if (e != cudaSuccess) return set_error(BSA_ERR_CUDA, std::string("eviction select launch: ") + cudaGetErrorString(e));
+  int st = launch_dependent("eviction select launch", select_kernel, unsigned(rows) * unsigned(C), kSelThreads,
+                            size_t(std::min(per, kKeysInSmem)) * 4, unsigned(C), stream, p, C);
+  if (st != BSA_OK) return st;
   const int tiles = (p.n + kMoveThreads - 1) / kMoveThreads;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(rows) * unsigned(tiles), 1, 1);
-  cfg.blockDim = dim3(kMoveThreads, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = d == 128 ? cudaLaunchKernelEx(&cfg, move_kernel<128>, p, tiles) : cudaLaunchKernelEx(&cfg, move_kernel<64>, p, tiles);
-  if (e != cudaSuccess) return set_error(BSA_ERR_CUDA, std::string("eviction move launch: ") + cudaGetErrorString(e));
-  return BSA_OK;
+  const unsigned grid = unsigned(rows) * unsigned(tiles);
+  return d == 128 ? launch_dependent("eviction move launch", move_kernel<128>, grid, kMoveThreads, 0, 1, stream, p, tiles)
+                  : launch_dependent("eviction move launch", move_kernel<64>, grid, kMoveThreads, 0, 1, stream, p, tiles);
 }
 
 }  // namespace evict

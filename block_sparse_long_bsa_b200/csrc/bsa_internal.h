@@ -71,6 +71,32 @@ int set_error(int status, const std::string& msg);
 // BSA_OK if the layout is on the current device, else an error (bsa_api.cpp).
 int check_layout_device(const bsa_layout* layout);
 
+// Launch with the attribute of programmatic dependent launch (see grid_wait in
+// bsa_device.cuh), in clusters of `cluster` blocks where that is above 1.
+#ifdef __CUDACC__
+template <class F, class... A>
+int launch_dependent(const char* what, F kern, unsigned grid, unsigned threads, size_t smem, unsigned cluster,
+                     cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  if (e != cudaSuccess) return set_error(BSA_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+  return BSA_OK;
+}
+#endif
+
 // Host layout compiler (bsa_layout.cpp).  Fills every host array and max_row, max_segs.
 int compile_layout(const bsa_pattern& spec, int n, int B, int L, bsa_layout* out);
 

@@ -155,9 +155,6 @@ struct Shape {
   static_assert(kKS == 2, "s_full doubles as the release of a K slot");
 };
 
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -230,7 +227,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
     return;
   }
-  grid_release();
   // the later layout rows' units last: most of them have nothing to do
   const int run = blockIdx.x % p.S;
   const int unit = blockIdx.x / p.S;
@@ -261,6 +257,27 @@ __global__ void __launch_bounds__(kThreads, 2)
   Run* s_run = reinterpret_cast<Run*>(smem + S::kOffRun);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Ctl ctl{abort_flag, p.status, kWaitNs};
+  if (threadIdx.x == 0) {
+    mbar_init(bQFull, 1);
+    for (int s = 0; s < kKS; ++s) mbar_init(bK0 + 8u * s, 1);
+    for (int s = 0; s < kVS; ++s) mbar_init(bV0 + 8u * s, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bS0 + 8u * s, 1);
+      mbar_init(bP0 + 8u * s, 32 * warps);
+    }
+    for (int s = 0; s < kVS; ++s) mbar_init(bO0 + 8u * s, 1);
+    mbar_init(bDrain, 1);
+    *abort_flag = 0;
+    *s_flag = 0;
+    fence_barrier_init();
+    tma_prefetch(&tmQ);
+    tma_prefetch(&tmK);
+    tma_prefetch(&tmV);
+  }
+  grid_wait();                                    // nothing of the caller's is read or written before this
+  // Only now may kernel 2 start: it reads the caller's arrays before its own
+  // wait, and what wrote them has ended only from here on.
+  grid_release();
 
   if constexpr (TREE) {
     // a later layout row has rows only if the tree is deep enough to reach it
@@ -296,18 +313,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       r.go = 1;
     }
     *s_run = r;
-    *s_flag = 0;
-    mbar_init(bQFull, 1);
-    for (int s = 0; s < kKS; ++s) mbar_init(bK0 + 8u * s, 1);
-    for (int s = 0; s < kVS; ++s) mbar_init(bV0 + 8u * s, 1);
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(bS0 + 8u * s, 1);
-      mbar_init(bP0 + 8u * s, 32 * warps);
-    }
-    for (int s = 0; s < kVS; ++s) mbar_init(bO0 + 8u * s, 1);
-    mbar_init(bDrain, 1);
-    *abort_flag = 0;
-    fence_barrier_init();
   }
   __syncthreads();
   const Run r = *s_run;
@@ -601,7 +606,7 @@ __device__ __forceinline__ int join_runs(const Params& p, int unit, int row, flo
     const int n = min(32, p.S - s0);
     const float* src = p.part_o + ((size_t(unit) * p.S + s0) * p.cap + row) * HD + lane * DPL;
     const size_t step = size_t(p.cap) * HD;
-    constexpr int U = 8;                 // runs in flight; one that wrote nothing is not read
+    constexpr int U = 4;                 // runs in flight; one that wrote nothing is not read
     for (int x0 = 0; x0 < n; x0 += U) {
       float v[U][DPL];
 #pragma unroll
@@ -669,6 +674,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 3) join_step_kernel(const Par
   __shared__ float s_m[32], s_l[32];
   __shared__ int s_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_release();
   if (int(blockIdx.x) < row_blocks) {
     const int f = blockIdx.x * kJoinWarps + warp;
     const int b = min(f, heads - 1) / p.H, t = p.lengths[b];
@@ -797,6 +803,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) join_tree_kernel(const Par
   __shared__ int s_path[kJoinWarps][kMaxT];       // ancestors from the token up to its root
   __shared__ float s_sc[kJoinWarps][kMaxT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_release();
   const int tb = (p.T + kJoinWarps - 1) / kJoinWarps;
   const int f = blockIdx.x / tb, i = blockIdx.x % tb * kJoinWarps + warp;
   const int b = f / p.H, hh = f - b * p.H;
@@ -928,23 +935,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) join_tree_kernel(const Par
 
 // ------------------------------------------------------------ host side
 
-// Kernel 2 is launched while kernel 1 still runs and waits for its end on the device.
-template <class F, class... A>
-int launch_after(const char* what, F kern, unsigned grid, unsigned threads, cudaStream_t s, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-  if (e != cudaSuccess) return set_error(BSA_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
-  return BSA_OK;
-}
-
 struct Call {
   const void* q;
   const void* k_cache;
@@ -979,17 +969,18 @@ int launch(const Call& c, const Params& p) {
   if (st == BSA_OK) st = tmap::encode_rows(&mk, c.k_cache, p.num_pages * p.hkv, BLK, HD, kChunk);
   if (st == BSA_OK) st = tmap::encode_rows(&mv, c.v_cache, p.num_pages * p.hkv, BLK, HD, kChunk);
   if (st != BSA_OK) return st;
-  kern<<<unsigned(c.plan.units) * unsigned(c.plan.S), kThreads, smem, c.stream>>>(mq, mk, mv, p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return set_error(BSA_ERR_CUDA, std::string("paged attention launch: ") + cudaGetErrorString(e));
+  st = launch_dependent("paged attention launch", kern, unsigned(c.plan.units) * unsigned(c.plan.S), kThreads, smem, 1,
+                        c.stream, mq, mk, mv, p);
+  if (st != BSA_OK) return st;
   if constexpr (TREE) {
     const unsigned tb = unsigned(p.T + kJoinWarps - 1) / kJoinWarps;
-    return launch_after("tree join launch", join_tree_kernel<BLK, HD>, unsigned(c.heads) * tb, kJoinWarps * 32, c.stream, p);
+    return launch_dependent("tree join launch", join_tree_kernel<BLK, HD>, unsigned(c.heads) * tb, kJoinWarps * 32, 0, 1,
+                            c.stream, p);
   } else {
     const int row_blocks = (c.heads + kJoinWarps - 1) / kJoinWarps;
     const unsigned grid = unsigned(row_blocks) + unsigned(c.batch * c.plan.hg) * unsigned(p.tiles);
-    return launch_after("step join launch", join_step_kernel<BLK, HD>, grid, kJoinWarps * 32, c.stream, p, c.heads,
-                        row_blocks);
+    return launch_dependent("step join launch", join_step_kernel<BLK, HD>, grid, kJoinWarps * 32, 0, 1, c.stream, p,
+                            c.heads, row_blocks);
   }
 }
 

@@ -160,7 +160,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
     return;
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t sQ = base, sK = base + S::kOffK, bar0 = base + S::kOffBar;
   const uint32_t bQFull0 = bar0, bQFree0 = bQFull0 + 8u * kQSlots, bKFull0 = bQFree0 + 8u * kQSlots,
                  bSFull0 = bKFull0 + 8u * kKSlots, bSFree0 = bSFull0 + 8u * kSBufs, bItem0 = bSFree0 + 8u * kSBufs,
@@ -194,6 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  grid_wait();                                   // nothing of the caller's is read or written before this
+  grid_release();
 
   // Items with kept blocks are counted by k, their tiles over all of them by t:
   // item k uses Q slot k % 2 and ring entry k % 8, tile t K slot and S buffer t % 4.
@@ -477,6 +478,7 @@ __global__ void __launch_bounds__(kAddThreads) add_rows_kernel(const Params p) {
   const int kvl = blockIdx.x / per, j0 = (blockIdx.x - kvl * per) * SL;
   const int sl = threadIdx.x / BLK, kl = threadIdx.x % BLK;
   const int u = (j0 + sl) * BLK + kl;
+  grid_release();
   float sum = 0.f;
 #pragma unroll 1
   for (int x0 = 0; x0 < p.upk; x0 += kUnits) {
@@ -499,7 +501,7 @@ __global__ void __launch_bounds__(kAddThreads) add_rows_kernel(const Params p) {
       }
     }
     __syncthreads();
-    if (x0 == 0) asm volatile("griddepcontrol.wait;" ::: "memory");   // the sums are in memory from here on
+    if (x0 == 0) grid_wait();              // the sums are in memory from here on
     int off = 0;
 #pragma unroll 1
     for (int x = 0; x < units; ++x) {
@@ -612,21 +614,13 @@ int launch(const void* q, const void* k, int kv_heads, Params p, const bsa_layou
   for (p.kv0 = 0; p.kv0 < kv_heads; p.kv0 += strip) {
     p.kvs = std::min(strip, kv_heads - p.kv0);
     p.items = uint32_t(p.kvs) * uint32_t(p.upk) * uint32_t(p.nb);
-    kern<<<std::min(p.items, unsigned(n_sm)), kThreads, S::kSmem, stream>>>(mq, mk, p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return set_error(BSA_ERR_CUDA, std::string("prompt weights launch: ") + cudaGetErrorString(e));
-    cudaLaunchConfig_t cfg = {};
+    st = launch_dependent("prompt weights launch", kern, std::min(p.items, unsigned(n_sm)), kThreads, S::kSmem, 1, stream,
+                          mq, mk, p);
+    if (st != BSA_OK) return st;
     constexpr int SL = kAddThreads / BLK;
-    cfg.gridDim = dim3(unsigned(p.kvs) * unsigned((p.nb + SL - 1) / SL), 1, 1);
-    cfg.blockDim = dim3(kAddThreads, 1, 1);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, add_rows_kernel<BLK>, p);
-    if (e != cudaSuccess) return set_error(BSA_ERR_CUDA, std::string("weights sum launch: ") + cudaGetErrorString(e));
+    st = launch_dependent("weights sum launch", add_rows_kernel<BLK>, unsigned(p.kvs) * unsigned((p.nb + SL - 1) / SL),
+                          kAddThreads, 0, 1, stream, p);
+    if (st != BSA_OK) return st;
   }
   return BSA_OK;
 }
