@@ -60,10 +60,12 @@ constexpr float kLn2 = 0.693147180559945309f;
 constexpr uint64_t kWaitNs = 1000000000ull, kDrainNs = 200000000ull;
 
 // Runs of a unit: as many CTAs as the GPU holds at once (two on each of 148
-// SMs) shared out over the units, and no run longer than kRunChunks, so that
-// sequences of other lengths and the end of the grid level out.
+// SMs) shared out over the units, rounded down (8 runs a unit, 512 CTAs, took
+// 114 us for 64-token trees over 8 x 16K where 4, 256 CTAs, took 106), and no run
+// longer than kRunChunks, so that sequences of other lengths level out (16 x 16K
+// step: 2 runs of 128 chunks 176 us, 4 of 64 169, 8 of 32 176).
 constexpr int kSlots = 2 * 148;
-constexpr int kRunChunks = 32;
+constexpr int kRunChunks = 64;
 
 struct Plan {
   int hg;          // head groups of a sequence: key/value heads, or query heads when routes differ by head
@@ -155,6 +157,21 @@ struct Shape {
   static_assert(kKS == 2, "s_full doubles as the release of a K slot");
 };
 
+// Two fp32 lanes at once, each rounded as the scalar instruction would.
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c) {
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\tmov.b64 rc, {%5, %5};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
+  asm("{\n\t.reg .b64 ra, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rd, {%0, %1};\n\t"
+      "add.rn.f32x2 rd, rd, ra;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "+f"(d0), "+f"(d1)
+      : "f"(a0), "f"(a1));
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -213,6 +230,13 @@ __device__ __forceinline__ int deepest(const int32_t* parents, int T, volatile i
   if (i < T) atomicMax(most, int(depth[i]));
   __syncthreads();
   return *most;
+}
+
+// Does row `at` of the layout keep all of the first `blocks` key blocks?  Its
+// columns ascend, so one entry tells.
+__device__ __forceinline__ bool keeps_all(const Params& p, size_t at, int blocks) {
+  const int start = p.row_ptr[at];
+  return blocks == 0 || (p.row_ptr[at + 1] - start >= blocks && p.col_idx[start + blocks - 1] == blocks - 1);
 }
 
 template <int BLK, int HD, bool TREE>
@@ -274,47 +298,72 @@ __global__ void __launch_bounds__(kThreads, 2)
     tma_prefetch(&tmK);
     tma_prefetch(&tmV);
   }
+  if (warp == 1) {
+    tmem_alloc(base + S::kOffMisc, S::kTmemCols);
+    tmem_relinquish();
+  }
   grid_wait();                                    // nothing of the caller's is read or written before this
   // Only now may kernel 2 start: it reads the caller's arrays before its own
   // wait, and what wrote them has ended only from here on.
   grid_release();
 
+  bool skip = false;
   if constexpr (TREE) {
     // a later layout row has rows only if the tree is deep enough to reach it
     if (grp > 0) {
       const int len = p.lengths[b];
       const int need = (len / BLK + grp) * BLK - len;
-      if (len < 0 || len > p.n || need > p.T - 1) return;
-      const int most = deepest(p.parents + size_t(b) * p.T, p.T, reinterpret_cast<volatile int8_t*>(smem + S::kOffJump),
-                               reinterpret_cast<volatile int8_t*>(smem + S::kOffDepth),
-                               reinterpret_cast<int*>(smem + S::kOffMisc + 12));
-      if (need > most) return;
+      skip = len < 0 || len > p.n || len / BLK + grp >= p.nb || need > p.T - 1;
+      if (!skip)
+        skip = need > deepest(p.parents + size_t(b) * p.T, p.T, reinterpret_cast<volatile int8_t*>(smem + S::kOffJump),
+                              reinterpret_cast<volatile int8_t*>(smem + S::kOffDepth),
+                              reinterpret_cast<int*>(smem + S::kOffMisc + 12));
+      // Where this layout row and the tree's first both keep all cached blocks,
+      // their rows read the same keys: the first one's runs serve both (a
+      // whole cache that a tree straddles two blocks of is read once, not twice).
+      if (!skip) {
+        const size_t at = size_t(f0 % p.L) * p.nb + len / BLK;
+        const int blocks = (len + BLK - 1) / BLK;
+        skip = keeps_all(p, at, blocks) && keeps_all(p, at + grp, blocks);
+      }
     }
   }
-  if (threadIdx.x == 0) {
+  // The run's place in its list, found by the warp that loads it: runs are cut
+  // from the row's length as the layout has it, so that the entries of a run
+  // are fetched at the same time as the row's last ones, which say how many
+  // blocks lie before the end of the cache.
+  int cols = 0, have = 0;                         // lane x holds list entry have + x
+  if (warp == 0) {
     Run r{};
     const int t = p.lengths[b];
     const int ctx = TREE ? t : t + 1;             // cached keys that exist
-    const int row = TREE ? t / BLK + grp : t / BLK;
-    if ((TREE ? t >= 0 && t <= p.n : t >= 0 && t < p.n) && row < p.nb) {
+    const int row = t / BLK + grp;
+    if (!skip && (TREE ? t >= 0 && t <= p.n : t >= 0 && t < p.n) && row < p.nb) {
       const size_t at = size_t(f0 % p.L) * p.nb + row;
       r.start = p.row_ptr[at];
-      int len = p.row_ptr[at + 1] - r.start, col = 0;
-      while (len > 0 && (col = p.col_idx[r.start + len - 1]) * BLK >= ctx) --len;   // at most groups + 1 steps
+      const int full = p.row_ptr[at + 1] - r.start;
+      r.c0 = int(int64_t(full) * CPB * run / p.S);
+      have = r.c0 / CPB;
+      cols = have + lane < full ? p.col_idx[r.start + have + lane] : 0;
+      // a row's blocks ascend to its own: at most `groups` of them, the last, lie at or past the end
+      const int end = lane < full ? p.col_idx[r.start + full - 1 - lane] : -1;
+      const int len = full - __popc(__ballot_sync(0xffffffffu, end >= 0 && end * BLK >= ctx));
       if (len > 0) {
+        const int col = __shfl_sync(0xffffffffu, end, full - len);
         const int rem = min(BLK, ctx - col * BLK);
         const int in_last = (rem + kChunk - 1) / kChunk;
-        const int chunks = (len - 1) * CPB + in_last;
-        r.last = chunks - 1;
+        r.last = (len - 1) * CPB + in_last - 1;
         r.tail = rem - (in_last - 1) * kChunk;
-        r.c0 = int(int64_t(chunks) * run / p.S);
-        r.c1 = int(int64_t(chunks) * (run + 1) / p.S);
+        r.c1 = min(int(int64_t(full) * CPB * (run + 1) / p.S), r.last + 1);
       }
       r.go = 1;
     }
-    *s_run = r;
+    if (lane == 0) *s_run = r;
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
   const Run r = *s_run;
   const int nch = r.c1 - r.c0;
   const size_t part = (size_t(unit) * p.S + run) * p.cap;
@@ -324,46 +373,42 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int x = threadIdx.x; x < vr; x += kThreads) p.part_ml[part + x] = make_float2(-INFINITY, 0.f);
       if (threadIdx.x == 0) p.part_flag[size_t(unit) * p.S + run] = 0;
     }
+    if (warp == 1) tmem_dealloc(tmem, S::kTmemCols);
     return;
   }
-  if (warp == 1) {
-    tmem_alloc(base + S::kOffMisc, S::kTmemCols);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_holder;
 
   if (warp == 0) {
     // ================================================================ loads
-    if (lane == 0) {
+    const bool leader = elect_one();
+    if (leader) {
       mbar_expect_tx(bQFull, S::kQBytes);
       if constexpr (HD == 128) tma_load_4d(sQ, &tmQ, bQFull, 0, mt * kTileM, 0, bh);
       else tma_load_3d(sQ, &tmQ, bQFull, 0, mt * kTileM, bh);
     }
-    const int e0 = r.c0 / CPB, e1 = (r.c1 - 1) / CPB + 1;   // list entries of the run
-    int have = e0, page_of = 0, flag = 0;                   // lane x holds the page of entry have + x
-    auto fetch = [&](int first) {
-      have = first;
-      const int e = first + lane;
+    const int e1 = (r.c1 - 1) / CPB + 1;          // past the run's last list entry
+    int page_of = 0, flag = 0;                    // lane x holds the page of entry have + x
+    auto pages = [&]() {
       page_of = 0;
-      if (e < e1) {
-        const int pg = p.page_table[size_t(b) * p.max_blocks + p.col_idx[r.start + e]];
+      if (have + lane < e1) {
+        const int pg = p.page_table[size_t(b) * p.max_blocks + cols];
         if (pg >= 0 && pg < p.num_pages) page_of = pg;
         else flag = 1;                   // page 0 is read in its place and the rows are refused
       }
     };
-    fetch(e0);
+    pages();
     int kc = 0, vc = 0;
     auto page_at = [&](int q) -> int {
       const int e = (r.c0 + q) / CPB;
-      if (e - have >= 32) fetch(e);
+      if (e - have >= 32) {
+        have = e;
+        cols = have + lane < e1 ? p.col_idx[r.start + have + lane] : 0;
+        pages();
+      }
       return __shfl_sync(0xffffffffu, page_of, e - have);
     };
     auto load_k = [&](int q, int page) -> bool {
       if (q >= kKS && !__all_sync(0xffffffffu, ctl.wait(bSFull(q), parS(q - kKS)))) return false;
-      if (lane == 0) {
+      if (leader) {
         mbar_expect_tx(bKFull(q), S::kTileBytes);
         tma_load_kv<HD>(sK + (q % kKS) * S::kTileBytes, &tmK, bKFull(q), ((r.c0 + q) % CPB) * kChunk,
                         page * p.hkv + hk);
@@ -373,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
     auto load_v = [&](int q, int page) -> bool {
       if (q >= kVS && !__all_sync(0xffffffffu, ctl.wait(bODone(q), parV(q - kVS)))) return false;
-      if (lane == 0) {
+      if (leader) {
         mbar_expect_tx(bVFull(q), S::kTileBytes);
         tma_load_kv<HD>(sV + (q % kVS) * S::kTileBytes, &tmV, bVFull(q), ((r.c0 + q) % CPB) * kChunk,
                         page * p.hkv + hk);
@@ -398,48 +443,55 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   } else if (warp == 1) {
     // ================================================================ products
-    if (lane == 0) {
-      constexpr uint64_t kFixK = sw128_fixed(16, 1024), kFixV = sw128_fixed(S::kAtomKV, 1024);
-      const uint32_t q_lo = uint32_t(kFixK) + (sQ >> 4), k_lo = uint32_t(kFixK) + (sK >> 4);
-      const uint32_t v_lo = uint32_t(kFixV) + (sV >> 4);
-      constexpr uint32_t kHiK = uint32_t(kFixK >> 32), kHiV = uint32_t(kFixV >> 32);
-      auto issue_qk = [&](int c) -> bool {
-        if (!ctl.wait(bKFull(c), parK(c))) return false;
-        tc_fence_after();
-        const uint32_t d = tmem + S::kColS + (c & 1) * kChunk;
-        const uint32_t kb = k_lo + uint32_t(c % kKS) * (S::kTileBytes >> 4);
+    const bool leader = elect_one();
+    constexpr uint64_t kFixK = sw128_fixed(16, 1024), kFixV = sw128_fixed(S::kAtomKV, 1024);
+    const uint32_t q_lo = uint32_t(kFixK) + (sQ >> 4), k_lo = uint32_t(kFixK) + (sK >> 4);
+    const uint32_t v_lo = uint32_t(kFixV) + (sV >> 4);
+    constexpr uint32_t kHiK = uint32_t(kFixK >> 32), kHiV = uint32_t(kFixV >> 32);
+    auto issue_qk = [&](int c) -> bool {
+      if (!__all_sync(0xffffffffu, ctl.wait(bKFull(c), parK(c)))) return false;
+      tc_fence_after();
+      const uint32_t d = tmem + S::kColS + (c & 1) * kChunk;
+      const uint32_t kb = k_lo + uint32_t(c % kKS) * (S::kTileBytes >> 4);
+      if (leader) {
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
           mma_ss(d, desc_from(q_lo + ((kk >> 2) * S::kAtomQ + (kk & 3) * 32) / 16, kHiK),
                  desc_from(kb + ((kk >> 2) * S::kAtomKV + (kk & 3) * 32) / 16, kHiK), S::kIdescQK, kk > 0 ? 1u : 0u);
         tc_commit(bSFull(c));
-        return true;
-      };
-      auto issue_pv = [&](int c) -> bool {
-        if (!ctl.wait(bVFull(c), parV(c))) return false;
-        if (!ctl.wait(bPFull(c), parS(c))) return false;
-        tc_fence_after();
-        const uint32_t pa = tmem + S::kColS + (c & 1) * kChunk;
-        const uint32_t vb = v_lo + uint32_t(c % kVS) * (S::kTileBytes >> 4);
+      }
+      __syncwarp();
+      return true;
+    };
+    auto issue_pv = [&](int c) -> bool {
+      if (!__all_sync(0xffffffffu, ctl.wait(bVFull(c), parV(c)) && ctl.wait(bPFull(c), parS(c)))) return false;
+      tc_fence_after();
+      const uint32_t pa = tmem + S::kColS + (c & 1) * kChunk;
+      const uint32_t vb = v_lo + uint32_t(c % kVS) * (S::kTileBytes >> 4);
+      if (leader) {
 #pragma unroll
-        for (int part2 = 0; part2 < 2; ++part2)          // P rounded, then the rest of it
+        for (int part2 = 0; part2 < 2; ++part2)            // P's upper bits, then the rest of it
 #pragma unroll
           for (int kk = 0; kk < kChunk / 16; ++kk)
             mma_ts(tmem + S::kColO, pa + part2 * 32 + kk * 8, desc_from(vb + kk * 16 * 128 / 16, kHiV), S::kIdescPV,
                    (c > 0 || part2 > 0 || kk > 0) ? 1u : 0u);
         tc_commit(bODone(c));
-        return true;
-      };
-      bool ok = ctl.wait(bQFull, 0);
-      tc_fence_after();
-      if (ok) ok = issue_qk(0);
-      for (int c = 0; c < nch && ok; ++c) {
-        if (c + 1 < nch) ok = issue_qk(c + 1);
-        if (ok) ok = issue_pv(c);
       }
+      __syncwarp();
+      return true;
+    };
+    bool ok = __all_sync(0xffffffffu, ctl.wait(bQFull, 0));
+    tc_fence_after();
+    if (ok) ok = issue_qk(0);
+    for (int c = 0; c < nch && ok; ++c) {
+      if (c + 1 < nch) ok = issue_qk(c + 1);
+      if (ok) ok = issue_pv(c);
+    }
+    if (leader) {
       tc_commit(bDrain);
       wait_drain(bDrain, 0, kDrainNs);
     }
+    __syncwarp();
   } else if ((warp & 3) < warps) {
     // ================================================================ softmax, one row per thread
     const int q4 = warp & 3;
@@ -490,14 +542,15 @@ __global__ void __launch_bounds__(kThreads, 2)
       float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
       for (int x = 0; x < kChunk; x += 4) {
-        sv[x] = ex2(fmaf(sv[x], sl2, neg_m));
-        sv[x + 1] = ex2(fmaf(sv[x + 1], sl2, neg_m));
-        sv[x + 2] = ex2(fmaf(sv[x + 2], sl2, neg_m));
-        sv[x + 3] = ex2(fmaf(sv[x + 3], sl2, neg_m));
-        s0 += sv[x];
-        s1 += sv[x + 1];
-        s2 += sv[x + 2];
-        s3 += sv[x + 3];
+        float x0, x1, x2, x3;
+        fma2(x0, x1, sv[x], sv[x + 1], sl2, neg_m);
+        fma2(x2, x3, sv[x + 2], sv[x + 3], sl2, neg_m);
+        sv[x] = ex2(x0);
+        sv[x + 1] = ex2(x1);
+        sv[x + 2] = ex2(x2);
+        sv[x + 3] = ex2(x3);
+        add2(s0, s1, sv[x], sv[x + 1]);
+        add2(s2, s3, sv[x + 2], sv[x + 3]);
       }
       l = l * alpha + ((s0 + s1) + (s2 + s3));
       if (c > 0 && __any_sync(0xffffffffu, need && mine)) {
@@ -841,7 +894,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) join_tree_kernel(const Par
     if (j >= blk0) keeps = 1u << (j - blk0);
   }
   keeps = __reduce_or_sync(0xffffffffu, keeps);
-  const int grp = blk - blk0;
+  int grp = blk - blk0;                           // whose runs the row reads: see kernel 1
+  if (live && !bad && grp > 0) {
+    const int blocks = (len + BLK - 1) / BLK;
+    if (keeps_all(p, at, blocks) && keeps_all(p, at - grp, blocks)) grp = 0;
+  }
   // scores of the ancestors: 8 lanes a key, four keys at a time
   const int sub = lane >> 3, pc = lane & 7;
   const int kvh = b * p.hkv + hh / (p.H / p.hkv);

@@ -129,13 +129,6 @@ __device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
       : "+f"(d0), "+f"(d1)
       : "f"(a0), "f"(a1));
 }
-// True in one thread of the warp, which is the same one every time.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
-
 // Waits for the loads of TMEM into v; the registers are operands so that no
 // use of them is moved before it while other loads are in flight.
 __device__ __forceinline__ void wait_ld32(float* v) {
