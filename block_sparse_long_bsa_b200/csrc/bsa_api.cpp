@@ -378,7 +378,8 @@ int bsa_get_status(const bsa_layout* layout, void* stream) {
   if (word & bsa::kStatusTimeout)
     return set_error(BSA_ERR_DEVICE_TIMEOUT, "a device-side wait ran out; the kernel returned early");
   if (word & bsa::kStatusBadIndex)
-    return set_error(BSA_ERR_SHAPE, "a decode position or page number was out of range; its row got o = 0");
+    return set_error(BSA_ERR_SHAPE, "a position, length, parent or page number was out of range; its rows got o = 0 "
+                                    "(an eviction leaves its sequence as it was)");
   return BSA_OK;
 }
 

@@ -75,9 +75,13 @@ __device__ __forceinline__ int cluster_rank() {
 }
 // All threads of all blocks of the cluster; shared memory written before it is
 // seen by the others after it.
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
 }
 __device__ __forceinline__ uint32_t peer_addr(const void* p, int rank) {
   uint32_t a;
@@ -114,32 +118,35 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
   reinterpret_cast<int4*>(hist)[tid] = make_int4(0, 0, 0, 0);
 #pragma unroll
   for (int d = 0; d < 3; ++d) reinterpret_cast<int4*>(sums[d])[tid] = make_int4(0, 0, 0, 0);
+  if (tid == 0) {
+    s_bad = 0;
+    s_newest = INT32_MIN;
+  }
+  cluster_sync();                                // every block's sums are zero
   grid_wait();                                   // nothing of the caller's is read or written before this
   grid_release();
   const int len = p.lengths[b];
   const float* w = p.weights + size_t(row) * p.stride;
   const int32_t* tok = p.tokens ? p.tokens + size_t(row) * p.stride : nullptr;
-  if (tid == 0) {
-    s_bad = len < 0 || len > p.n;
-    s_newest = INT32_MIN;
+  auto refuse = [&]() {
+    if (tid == 0 && rank == 0) {
+      p.meta[row] = make_int4(0, 0, 1, 1);
+      atomicOr(p.status, kStatusBadIndex);
+    }
+  };
+  if (len < 0 || len > p.n) {
+    refuse();
+    return;
   }
-  __syncthreads();
-  if (!s_bad && len > p.budget) {
-    // every block of the cluster looks at all pages, so all agree
+  if (len > p.budget) {
+    // every block of the cluster looks at all pages, so all agree; the answer
+    // is read once the keys are there
     bool bad = false;
     for (int j = tid; j < (len + p.B - 1) / p.B; j += kSelThreads) {
       const int pg = p.page_table[size_t(b) * p.max_blocks + j];
       bad |= pg < 0 || pg >= p.num_pages;
     }
     if (bad) s_bad = 1;
-  }
-  __syncthreads();
-  if (s_bad) {
-    if (tid == 0 && rank == 0) {
-      p.meta[row] = make_int4(0, 0, 1, 1);
-      atomicOr(p.status, kStatusBadIndex);
-    }
-    return;
   }
   const int per = (len + C * 32 - 1) / (C * 32) * 32;
   const int first = min(len, rank * per), end = min(len, first + per);
@@ -156,7 +163,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
     }
     m = __reduce_max_sync(0xffffffffu, m);
     if (lane == 0) atomicMax(&s_newest, m);
-    cluster_sync();                      // also: every block's sums are zero from here on
+    cluster_sync();
     newest = INT32_MIN;
 #pragma unroll 1
     for (int r = 0; r < C; ++r) newest = max(newest, ld_peer(peer_addr(&s_newest, r)));
@@ -167,7 +174,6 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
     cluster_sync();                      // the others may still be reading s_newest here
     return;
   }
-  if (!tok && C > 1) cluster_sync();     // every block's sums are zero
   const int64_t floor_tok = int64_t(newest) - p.recent;      // tokens above it are protected
   auto key_from = [&](int t, float x) -> uint32_t { return int64_t(t) > floor_tok ? 0xffffffffu : key_of(x); };
   auto make_key = [&](int s) -> uint32_t { return key_from(tok ? tok[s] : s, w[s]); };
@@ -188,6 +194,12 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
     }
   }
   auto key_at = [&](int s) -> uint32_t { return held ? s_keys[s - first] : make_key(s); };
+  __syncthreads();
+  if (s_bad) {
+    refuse();
+    if (C > 1) cluster_sync();           // the others may still be reading s_newest here
+    return;
+  }
 
   // ---- the budget-th largest key, from the highest digit down
   uint32_t prefix = 0, mask = 0;
@@ -289,7 +301,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
     return __ballot_sync(0xffffffffu, take);
   };
   int holes = 0, movers = 0, seen = ties;
-#pragma unroll 1
+#pragma unroll 4
   for (int s0 = lo; s0 < hi; s0 += 32) {
     const unsigned kept = kept_of(s0, seen);
     // slots of this ballot that lie below the budget
@@ -308,6 +320,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
     hole0 += ld_peer(peer_addr(&s_holes, r));
     mover0 += ld_peer(peer_addr(&s_movers, r));
   }
+  cluster_arrive();
   int32_t* const mv = p.movers + size_t(row) * p.cap;
   int32_t* const src = p.src + size_t(row) * p.cap;
   seen = ties;
@@ -324,7 +337,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
     hole0 += __popc(hb);
   }
   if (tid == 0 && rank == 0) p.meta[row] = make_int4(p.budget, newest, 0, 0);
-  cluster_sync();                        // no block ends while another may still read its shared memory
+  cluster_wait();                        // no block ends while another may still read its shared memory
 }
 
 template <int HD>

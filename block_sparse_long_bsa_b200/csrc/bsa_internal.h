@@ -106,7 +106,7 @@ constexpr int kColumnSegment = 16;
 
 // Device status bits.
 constexpr uint32_t kStatusTimeout = 1u;
-constexpr uint32_t kStatusBadIndex = 2u;   // a decode position or page number was out of range
+constexpr uint32_t kStatusBadIndex = 2u;   // a position, length, parent or page number was out of range
 // The status block that follows a layout's arrays holds the status word at
 // word 0 and, from byte 256 on, the work counters (kWorkCounters eager ones,
 // then kGraphCounters for captured calls), one per 128-byte line.  The

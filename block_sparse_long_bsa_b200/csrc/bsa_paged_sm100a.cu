@@ -723,7 +723,7 @@ __device__ __forceinline__ int find_block(const Params& p, size_t at, int j) {
 constexpr int kGroups = 4, kGroupKeys = 4 * kJoinWarps * 32, kTileKeys = kGroups * kGroupKeys;
 
 template <int BLK, int HD>
-__global__ void __launch_bounds__(kJoinWarps * 32, 3) join_step_kernel(const Params p, int heads, int row_blocks) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) join_step_kernel(const Params p, int heads, int row_blocks) {
   __shared__ float s_m[32], s_l[32];
   __shared__ int s_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

@@ -579,6 +579,85 @@ def test_tree_row_is_the_decode_step_of_its_path():
     lay.close()
 
 
+# ------------------------------------------------------------------ caches past 2^31 elements, shared pages
+
+def test_caches_whose_offsets_pass_32_bits():
+    """Step, tree and cut on pages at the far end of caches of 2.3e9 elements: the bits they give on small ones."""
+    n, B, batch, H, G, d, T = 1000, 64, 2, 4, 4, 128, 5
+    if torch.cuda.mem_get_info()[0] < 14 << 30:
+        pytest.skip("needs 14 GB of device memory")
+    lay = _layout(OL.BAND_GLOBAL, n, B, 1, dict(window=16, global_first=0))
+    kc, vc, table, th = _paged(batch, G, n, B, d, 210)
+    pages, far = kc.shape[0], 70000
+    assert far * G * B * d > 2 ** 31
+    big = [torch.empty((far, G, B, d), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for b, c in zip(big, (kc, vc)):
+        b[far - pages:] = c
+    table2 = table + (far - pages)
+    q, kt, vt = (to_device_bf16(x) for x in inputs.qkv_bits(batch * H, batch * G, T, d, seeds=(211, 212, 213)))
+    lens = torch.tensor([900, 640], dtype=torch.int32, device="cuda")
+    par = torch.tensor([[-1, 0, 0, 1, 3]] * batch, dtype=torch.int32, device="cuda")
+    got = []
+    for k, v, t in ((kc, vc, table), (big[0], big[1], table2)):
+        w = torch.zeros((batch * G, n), device="cuda")
+        tree = bsa.decode_tree(q, kt, vt, k, v, t, lens, par, lay)
+        step = bsa.decode_weights(q[:, 0].contiguous(), k, v, t, lens - 1, lay, batch, w)
+        cut = bsa.evict(k, v, t, lens, w, lay, 300, 10)
+        torch.cuda.synchronize()
+        got.append([*tree, *step, w, *cut, k[-pages:].clone(), v[-pages:].clone()])
+    bsa.bsa_get_status(lay.handle)
+    for a, b in zip(*got):
+        assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+    lay.close()
+
+
+def test_sequences_that_share_their_first_pages():
+    """A prefix that two sequences hold in the same pages: each gives what it gives with pages of its own."""
+    n, B, H, G, d, T = 640, 64, 4, 2, 64, 6
+    lay = _layout(OL.BAND_GLOBAL, n, B, 1, dict(window=10, global_first=0))
+    kc, vc, table, th = _paged(2, G, n, B, d, 220)
+    for c in (kc, vc):
+        c[table[1, :4].long()] = c[table[0, :4].long()]
+    shared = table.clone()
+    shared[1, :4] = table[0, :4]
+    q, kt, vt = (to_device_bf16(x) for x in inputs.qkv_bits(2 * H, 2 * G, T, d, seeds=(221, 222, 223)))
+    lens = torch.tensor([500, 300], dtype=torch.int32, device="cuda")
+    par = torch.tensor([[-1, 0, 1, 1, -1, 4]] * 2, dtype=torch.int32, device="cuda")
+    out = []
+    for t in (table, shared):
+        w = torch.zeros((2 * G, n), device="cuda")
+        out.append([*bsa.decode_tree(q, kt, vt, kc, vc, t, lens, par, lay),
+                    *bsa.decode_weights(q[:, 0].contiguous(), kc, vc, t, lens - 1, lay, 2, w), w])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+    lay.close()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_tree_that_straddles_blocks_of_a_whole_cache(d):
+    """Where every block is kept, rows of two or three layout rows share their runs: against the oracle, with the
+    cache ending at, before and behind a block's border."""
+    n, B, H, G, T = 500, 64, 4, 2, 90
+    lay = _layout(OL.BAND_GLOBAL, n, B, 1, dict(window=8, global_first=0))
+    sets = OL.kept_sets(OL.BAND_GLOBAL, n, B, 1, window=8, global_first=0)
+    par = np.array([list(range(-1, T - 1))], np.int32)
+    par[0, 70:] = 20
+    for length in (191, 192, 193, 250, 0):
+        kc, vc, table, th = _paged(1, G, n, B, d, 230)
+        _blank(kc, vc, th, B, [length])
+        q, kt, vt = (to_device_bf16(x) for x in inputs.qkv_bits(H, G, T, d, seeds=(231, 232, 233)))
+        o, lse = bsa.decode_tree(q, kt, vt, kc, vc, table, torch.tensor([length], dtype=torch.int32, device="cuda"),
+                                 torch.from_numpy(par).cuda(), lay)
+        torch.cuda.synchronize()
+        bsa.bsa_get_status(lay.handle)
+        kh, vh = np.nan_to_num(_np(kc)), np.nan_to_num(_np(vc))
+        o_ref, lse_ref = OC.tree(_np(q), _np(kt), _np(vt), kh, vh, th, [length], par, sets, B, d ** -0.5)
+        e_p = _e_p(d ** -0.5, d, _np(q), np.concatenate([kh.reshape(-1, d), _np(kt).reshape(-1, d)]), lse_ref)
+        _close_lse(_np(lse), lse_ref, e_p)
+        _close_o(_np(o), o_ref, e_p, np.concatenate([vh.reshape(-1, d), _np(vt).reshape(-1, d)]))
+    lay.close()
+
+
 # ------------------------------------------------------------------ how they are called
 
 def _small_tree(seed, stream=None):
