@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int x = 0; x < NQ32; ++x) {
           const int c = x * 32 + lane, tok = r.i * BLK + c % BLK;
-          w.lse[x] = tok < p.n ? p.lse[size_t(r.f0 + c / BLK) * p.n + tok] : INFINITY;
+          w.lse[x] = tok < p.n ? p.lse[size_t(r.f0 + c / BLK) * p.n + tok] : -INFINITY;
         }
       }
       return w;
@@ -254,7 +254,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       next = after;
       mine = theirs;
       if (len <= 0) continue;
-      // -lse log2 e of the item's query rows, -inf for one past the sequence's end
+      // -lse log2 e of the item's query rows.  One past the sequence's end counts as
+      // one without weight: its scores are 0 or, with an infinite key, NaN.
       float neg[NQ32];
       bool dead = false;
 #pragma unroll

@@ -187,6 +187,30 @@ def test_prompt_weights_of_rows_that_are_not_numbers_stay_in_their_columns():
     lay.close()
 
 
+@pytest.mark.parametrize("B,H", [(64, 1), (64, 2), (128, 1)])
+def test_prompt_weights_of_a_key_that_no_row_gives_weight(B, H):
+    """A key at minus infinity for every row that reads it gets a weight of 0, in a last block that the sequence
+    does not fill too: the block's rows past the end have no say."""
+    n, d = 450, 64
+    lay = _layout(OL.BAND_GLOBAL, n, B, 1, dict(window=1, global_first=0))
+    sets = OL.kept_sets(OL.BAND_GLOBAL, n, B, 1, window=1, global_first=0)
+    qb, kb, vb = inputs.qkv_bits(H, 1, n, d, seeds=(14, 15, 16))
+    q, k, v = (to_device_bf16(x) for x in (qb, kb, vb))
+    q[:, :, 0] = q[:, :, 0].abs() + 0.5
+    k[0, [100, 380, 400, 449], 0] = float("-inf")
+    _, lse = bsa.attention(q, k, v, lay)
+    lse_h = _np(lse)
+    assert np.isfinite(lse_h).all()
+    w = bsa.attention_weights(q, k, lse, lay)
+    torch.cuda.synchronize()
+    got = _np(w)
+    want = OC.prompt_weights(_np(q), _np(k), lse_h, sets, B, d ** -0.5)
+    e_p = _e_p(d ** -0.5, d, _np(q), np.nan_to_num(_np(k), neginf=0), lse_h)
+    assert (want[0, [100, 380, 400, 449]] == 0).all()
+    _close_w(got, want, e_p, lse_h)
+    lay.close()
+
+
 # ------------------------------------------------------------------ paged caches
 
 def _paged(batch, G, n, B, d, seed, spare=0):
