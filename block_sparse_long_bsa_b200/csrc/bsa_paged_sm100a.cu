@@ -182,12 +182,12 @@ __device__ __forceinline__ void bf16x2_to_f32(uint32_t w, float& lo, float& hi) 
   hi = __uint_as_float(w & 0xffff0000u);
 }
 
-// What cutting a probability's low 16 bits off leaves, and never 0: an
+// What cutting a probability's low 16 bits off leaves, and (least > 0) never 0: an
 // infinite value that the row reads then has the same sign in both products
 // (a rounded first part could leave a negative rest, and 0 * inf is NaN).
 // P itself being 0, where exp2 underflows, is 0 * inf in the definition too.
-__device__ __forceinline__ float rest_of(uint32_t bits) {
-  return fmaxf(__uint_as_float(bits) - __uint_as_float(bits & 0xffff0000u), 1e-30f);
+__device__ __forceinline__ float rest_of(uint32_t bits, float least) {
+  return fmaxf(__uint_as_float(bits) - __uint_as_float(bits & 0xffff0000u), least);
 }
 
 // What a CTA of kernel 1 works on, found by one thread and shared.
@@ -499,6 +499,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     const bool mine = row < vr;
     const uint32_t lane_base = tmem + (uint32_t(q4 * 32) << 16);
     const float sl2 = p.scale_log2;
+    // A row that the tile only has room for gets P = 0, not the 1 of its zero
+    // scores: a step's tile has 30 of them for 2 rows, and the tensor cores'
+    // power lowers the clocks (16 x 16K steps for seconds: 181 us each for 184).
+    const float least = mine ? 1e-30f : 0.f;
     float m2 = -INFINITY, l = 0.f;
     bool ok = true;
     for (int c = 0; c < nch; ++c) {
@@ -538,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         alpha = ex2(m2 - mb);
         m2 = mb;
       }
-      const float neg_m = m2 == -INFINITY ? 0.f : -m2;
+      const float neg_m = !mine ? -INFINITY : m2 == -INFINITY ? 0.f : -m2;
       float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
       for (int x = 0; x < kChunk; x += 4) {
@@ -574,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int e = 0; e < 16; ++e) {
           const uint32_t a = __float_as_uint(sv[x * 32 + 2 * e]), bb = __float_as_uint(sv[x * 32 + 2 * e + 1]);
           hi[e] = __byte_perm(a, bb, 0x7632);
-          lo[e] = pack_bf16(rest_of(a), rest_of(bb));
+          lo[e] = pack_bf16(rest_of(a, least), rest_of(bb, least));
         }
         tmem_st16(s_col + x * 16, hi);
         tmem_st16(s_col + 32 + x * 16, lo);
@@ -961,7 +965,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) join_tree_kernel(const Par
     float sum = 0.f;
     for (int x = lane; x < count; x += 32) {
       const float s = s_sc[warp][x];
-      // an ancestor that is not read is marked by NaN-free 0 and skipped below
+      // one that is not read gets 0 and, as 0 times its value may be NaN, is left out below
       const bool use = keeps >> ((len + count - 1 - x) / BLK - blk0) & 1u;
       const float w = use ? ex2(s - (all == -INFINITY ? 0.f : all)) : 0.f;
       s_sc[warp][x] = w;

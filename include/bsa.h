@@ -302,8 +302,9 @@ size_t bsa_decode_weights_workspace_bytes(const bsa_layout* layout, int batch, i
                                           int kv_heads, int d);
 
 /* A decode step that adds up the weights it gives: o and lse as bsa_decode
- * gives them (with P rounded nowhere before o), and for every key/value head
- * kv of sequence b and every cached token u that its query rows read
+ * gives them (P kept to within 2^-15 of itself, o rounded at its end), and for
+ * every key/value head kv of sequence b and every cached token u that its
+ * query rows read
  *   weights[(b*Hkv + kv) * weights_stride + u] += sum over the query rows f of
  *       kv that read u of exp(s_u - lse[f]).
  * Arguments and layouts as for bsa_decode; weights fp32, rows weights_stride
