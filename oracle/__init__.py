@@ -18,11 +18,14 @@ Modules:
   decode    -- one selected-page decode step through a page table.
   backward  -- the gradients of the masked softmax, written out.
   bsbr      -- BSBR's chunk states, meta weights and retrieval term.
+  cache     -- the weights that cached keys receive, the cut of a paged cache
+               by them and the attention of a drafted tree.
 
 Every function is pinned by a ``-m "not gpu"`` test against something other
 than itself (printed page values, closed forms, library routines, invariants,
 brute force): ``tests/test_oracle_layouts.py``,
 ``tests/test_oracle_attention.py``, ``tests/test_oracle_decode.py``,
-``tests/test_oracle_backward.py`` and ``tests/test_oracle_bsbr.py``.
+``tests/test_oracle_backward.py``, ``tests/test_oracle_bsbr.py`` and
+``tests/test_oracle_cache.py``.
 """
 from . import layouts, attention  # noqa: F401

@@ -2,7 +2,8 @@
 infrastructure): the weights that cached keys receive, the cut of a cache to a
 budget by them, and the attention of a tree of drafted tokens.
 
-Only ``tests/`` may call this module; the product path never does.
+Only ``tests/`` and ``__graft_entry__.smoke()`` may call this module; the
+product path never does.
 
 The operators stand beside selected-page decode ("BF1: A Causal Dyadic
 Sparse-Attention Retrofit for Efficient Long-Context Transformers", section 5)
