@@ -28,6 +28,19 @@
 // branch's infinity cannot reach another branch.  The step's kernel 2 also
 // turns the scores into weights, p = exp2(s scale log2 e - M) / L.
 //
+// At most 8 rows (every step of a grouped-query model, short trees) take the
+// products the other way round, keys as the rows of a tile:
+//   S^T = K Q^T,   O^T += V^T [P^T upper bits | rest]      (N = 16 both)
+// where more rows take 128 x 64 and twice 128 x d tiles for the same keys.  A
+// step is bound by memory either way, but the large tiles, nearly all of them
+// empty, kept the tensor cores 60 % busy, and a server's GPU runs at its power
+// limit: 16 x 16K steps that follow each other for seconds took 181 to 193 us
+// each with the clocks at 1.45 to 1.6 GHz, and take 162 at 1.8; a few at a
+// time 164 and 160.  (128 rows of S^T are 64 keys and whatever lies behind them in shared
+// memory, which nobody reads.)  With 8 rows both ways take the same time,
+// 41.1 and 42.0 us over 2 x 131K, 82.8 and 83.1 over 8 x 16K; with 1 row 28.0
+// and 29.2, 80.9 and 81.5.
+//
 // Roles of kernel 1 (192 threads, two CTAs per SM): warp 0 looks the pages up
 // and issues the TMA loads, warp 1 issues the products, warps 2-5 hold one
 // query row per thread.  Every wait is bounded, as in the forward.
@@ -53,7 +66,8 @@ using namespace ptx;
 constexpr int kThreads = 192;
 constexpr int kTileM = 128;            // query rows of a tile (tcgen05 M = 128)
 constexpr int kChunk = 64;             // keys per chunk
-constexpr int kKS = 2, kVS = 3;        // K and V slots in shared memory
+constexpr int kVS = 3;                 // V slots in shared memory
+constexpr int kFew = 8;                // query rows that the keys' side of a product can take
 constexpr int kMaxT = 128;             // drafted tokens at most
 constexpr float kRescaleThreshold = 8.0f;
 constexpr float kLn2 = 0.693147180559945309f;
@@ -133,28 +147,39 @@ struct Params {
   float scale_log2;
 };
 
-template <int BLK, int HD>
+template <int BLK, int HD, bool FEW>
 struct Shape {
   static constexpr int kCPB = BLK / kChunk;
-  static constexpr int kQBytes = kTileM * HD * 2;
+  static constexpr int kKS = FEW ? 3 : 2;                    // K slots, S buffers and P buffers
+  static constexpr int kRowsQ = FEW ? 2 * kFew : kTileM;
+  static constexpr int kQBytes = kRowsQ * HD * 2;
   static constexpr int kTileBytes = kChunk * HD * 2;
-  static constexpr int kAtomQ = kTileM * 128, kAtomKV = kChunk * 128;
+  static constexpr int kAtomQ = kRowsQ * 128, kAtomKV = kChunk * 128;
   static constexpr int kOffK = kQBytes;
   static constexpr int kOffV = kOffK + kKS * kTileBytes;
-  static constexpr int kOffBar = kOffV + kVS * kTileBytes;
-  // q_full, k_full[KS], v_full[VS], s_full[2], p_full[2], o_done[VS], drain
-  static constexpr int kNumBars = 1 + kKS + kVS + 2 + 2 + kVS + 1;
+  // Few rows: P^T as the second product's B operand, N-major and unswizzled:
+  // cores of 8 keys by 8 rows, 16 bytes a key; for 8 keys a core of P's upper
+  // bits, one of its rest and 32 bytes that keep a warp's writes off each other's banks.
+  static constexpr int kKeysP = 2 * 128 + 32, kPBytes = FEW ? kChunk / 8 * kKeysP : 0;
+  static constexpr int kOffP = kOffV + kVS * kTileBytes;
+  static constexpr int kOffMax = kOffP + kKS * kPBytes;      // row maxima [2][2][kFew], sums [2][kFew], moves [2][2]
+  static constexpr int kOffBar = kOffMax + (FEW ? 6 * kFew * 4 + 16 : 0);
+  // q_full, k_full[KS], v_full[VS], s_full[KS], p_full[KS], o_done[VS], drain; few rows: max moves[2], maxima[2], sums
+  static constexpr int kNumBars = 1 + kKS + kVS + kKS + kKS + kVS + 1 + (FEW ? 5 : 0);
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // TMEM address, abort flag, page flag, deepest token
   static constexpr int kOffRun = kOffMisc + 16;
   static constexpr int kOffJump = kOffRun + 32;              // the tree's walk, a byte a token
   static constexpr int kOffDepth = kOffJump + kMaxT;
   static constexpr int kSmem = kOffDepth + kMaxT;
-  static constexpr int kColS = 0, kColO = 2 * kChunk;
-  static constexpr uint32_t kTmemCols = 256;
-  static constexpr uint32_t kIdescQK = idesc_bf16(kTileM, kChunk, 0, 0);
-  static constexpr uint32_t kIdescPV = idesc_bf16(kTileM, HD, 0, 1);
-  static_assert(2 * kChunk + HD <= 256, "TMEM budget");
-  static_assert(kKS == 2, "s_full doubles as the release of a K slot");
+  static constexpr int kSCols = FEW ? 2 * kFew : kChunk;
+  static constexpr int kColS = 0, kColO = kKS * kSCols;
+  static constexpr uint32_t kTmemCols = FEW ? 64 : 256;
+  static constexpr uint32_t kIdescQK = idesc_bf16(kTileM, kSCols, 0, 0);
+  static constexpr uint32_t kIdescPV = FEW ? idesc_bf16(kTileM, 2 * kFew, 1, 1) : idesc_bf16(kTileM, HD, 0, 1);
+  static_assert(kColO + (FEW ? 2 * kFew : HD) <= int(kTmemCols), "TMEM budget");
+  static_assert(kOffBar % 8 == 0 && kOffP % 16 == 0, "alignment");
+  // Few rows: a product of 128 rows reads 8 KB past a 64-row operand (the next slot, or what follows the last)
+  static_assert(!FEW || kOffV + kVS * kTileBytes + kAtomKV <= 77 * 1024 || HD == 128, "inside the CTA's shared memory");
 };
 
 // Two fp32 lanes at once, each rounded as the scalar instruction would.
@@ -177,9 +202,38 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+// The largest of a warp's values, a NaN counting for nothing.
+__device__ __forceinline__ float warp_max(float x) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
+}
 __device__ __forceinline__ void bf16x2_to_f32(uint32_t w, float& lo, float& hi) {
   lo = __uint_as_float(w << 16);
   hi = __uint_as_float(w & 0xffff0000u);
+}
+
+// Eight consecutive fp32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+               "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+               "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+               "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+               : "memory");
+}
+// Fixed fields of a shared-memory descriptor without swizzle: `k_bytes` from
+// core to core along K, `row_bytes` along the rows.
+__host__ __device__ constexpr uint64_t flat_fixed(uint32_t k_bytes, uint32_t row_bytes) {
+  return (uint64_t((k_bytes >> 4) & 0x3FFFu) << 16) | (uint64_t((row_bytes >> 4) & 0x3FFFu) << 32) | (uint64_t(1) << 46);
 }
 
 // What cutting a probability's low 16 bits off leaves, and (least > 0) never 0: an
@@ -239,12 +293,12 @@ __device__ __forceinline__ bool keeps_all(const Params& p, size_t at, int blocks
   return blocks == 0 || (p.row_ptr[at + 1] - start >= blocks && p.col_idx[start + blocks - 1] == blocks - 1);
 }
 
-template <int BLK, int HD, bool TREE>
+template <int BLK, int HD, bool TREE, bool FEW>
 __global__ void __launch_bounds__(kThreads, 2)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV, const Params p) {
-  using S = Shape<BLK, HD>;
-  constexpr int CPB = S::kCPB;
+  using S = Shape<BLK, HD, FEW>;
+  constexpr int CPB = S::kCPB, kKS = S::kKS;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_addr(smem);
   if (base & 1023u) {                    // never expected: the swizzle needs 1024-byte aligned tiles
@@ -265,16 +319,15 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   const uint32_t sQ = base, sK = base + S::kOffK, sV = base + S::kOffV;
   const uint32_t bar0 = base + S::kOffBar;
-  const uint32_t bQFull = bar0, bK0 = bar0 + 8u, bV0 = bK0 + 8u * kKS, bS0 = bV0 + 8u * kVS, bP0 = bS0 + 16u,
-                 bO0 = bP0 + 16u, bDrain = bO0 + 8u * kVS;
+  const uint32_t bQFull = bar0, bK0 = bar0 + 8u, bV0 = bK0 + 8u * kKS, bS0 = bV0 + 8u * kVS, bP0 = bS0 + 8u * kKS,
+                 bO0 = bP0 + 8u * kKS, bDrain = bO0 + 8u * kVS, bMax = bDrain + 8u, bTop = bMax + 16u, bSum = bTop + 16u;
   auto bKFull = [&](int c) { return bK0 + 8u * (c % kKS); };
   auto bVFull = [&](int c) { return bV0 + 8u * (c % kVS); };
-  auto bSFull = [&](int c) { return bS0 + 8u * (c & 1); };
-  auto bPFull = [&](int c) { return bP0 + 8u * (c & 1); };
+  auto bSFull = [&](int c) { return bS0 + 8u * (c % kKS); };
+  auto bPFull = [&](int c) { return bP0 + 8u * (c % kKS); };
   auto bODone = [&](int c) { return bO0 + 8u * (c % kVS); };
   auto parK = [](int c) { return uint32_t(c / kKS) & 1u; };
   auto parV = [](int c) { return uint32_t(c / kVS) & 1u; };
-  auto parS = [](int c) { return uint32_t(c >> 1) & 1u; };
   volatile uint32_t* tmem_holder = reinterpret_cast<volatile uint32_t*>(smem + S::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kOffMisc + 4);
   volatile int* s_flag = reinterpret_cast<volatile int*>(smem + S::kOffMisc + 8);
@@ -285,12 +338,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     mbar_init(bQFull, 1);
     for (int s = 0; s < kKS; ++s) mbar_init(bK0 + 8u * s, 1);
     for (int s = 0; s < kVS; ++s) mbar_init(bV0 + 8u * s, 1);
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kKS; ++s) {
       mbar_init(bS0 + 8u * s, 1);
-      mbar_init(bP0 + 8u * s, 32 * warps);
+      mbar_init(bP0 + 8u * s, FEW ? 128 : 32 * warps);
     }
     for (int s = 0; s < kVS; ++s) mbar_init(bO0 + 8u * s, 1);
     mbar_init(bDrain, 1);
+    if constexpr (FEW)
+      for (int s = 0; s < 5; ++s) mbar_init(bMax + 8u * s, 2);
     *abort_flag = 0;
     *s_flag = 0;
     fence_barrier_init();
@@ -382,8 +437,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     const bool leader = elect_one();
     if (leader) {
       mbar_expect_tx(bQFull, S::kQBytes);
-      if constexpr (HD == 128) tma_load_4d(sQ, &tmQ, bQFull, 0, mt * kTileM, 0, bh);
-      else tma_load_3d(sQ, &tmQ, bQFull, 0, mt * kTileM, bh);
+#pragma unroll
+      for (int a = 0; a < HD / 64; ++a) tma_load_3d(sQ + a * S::kAtomQ, &tmQ, bQFull, a * 64, mt * kTileM, bh);
     }
     const int e1 = (r.c1 - 1) / CPB + 1;          // past the run's last list entry
     int page_of = 0, flag = 0;                    // lane x holds the page of entry have + x
@@ -407,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       return __shfl_sync(0xffffffffu, page_of, e - have);
     };
     auto load_k = [&](int q, int page) -> bool {
-      if (q >= kKS && !__all_sync(0xffffffffu, ctl.wait(bSFull(q), parS(q - kKS)))) return false;
+      if (q >= kKS && !__all_sync(0xffffffffu, ctl.wait(bSFull(q), parK(q - kKS)))) return false;
       if (leader) {
         mbar_expect_tx(bKFull(q), S::kTileBytes);
         tma_load_kv<HD>(sK + (q % kKS) * S::kTileBytes, &tmK, bKFull(q), ((r.c0 + q) % CPB) * kChunk,
@@ -448,27 +503,41 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t q_lo = uint32_t(kFixK) + (sQ >> 4), k_lo = uint32_t(kFixK) + (sK >> 4);
     const uint32_t v_lo = uint32_t(kFixV) + (sV >> 4);
     constexpr uint32_t kHiK = uint32_t(kFixK >> 32), kHiV = uint32_t(kFixV >> 32);
+    constexpr uint64_t kFixP = flat_fixed(S::kKeysP, 128);
+    const uint32_t p_lo = uint32_t(kFixP) + ((base + S::kOffP) >> 4);
+    constexpr uint32_t kHiP = uint32_t(kFixP >> 32);
     auto issue_qk = [&](int c) -> bool {
       if (!__all_sync(0xffffffffu, ctl.wait(bKFull(c), parK(c)))) return false;
       tc_fence_after();
-      const uint32_t d = tmem + S::kColS + (c & 1) * kChunk;
+      const uint32_t d = tmem + S::kColS + (c % kKS) * S::kSCols;
       const uint32_t kb = k_lo + uint32_t(c % kKS) * (S::kTileBytes >> 4);
       if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk)
-          mma_ss(d, desc_from(q_lo + ((kk >> 2) * S::kAtomQ + (kk & 3) * 32) / 16, kHiK),
-                 desc_from(kb + ((kk >> 2) * S::kAtomKV + (kk & 3) * 32) / 16, kHiK), S::kIdescQK, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < HD / 16; ++kk) {
+          const uint64_t qd = desc_from(q_lo + ((kk >> 2) * S::kAtomQ + (kk & 3) * 32) / 16, kHiK);
+          const uint64_t kd = desc_from(kb + ((kk >> 2) * S::kAtomKV + (kk & 3) * 32) / 16, kHiK);
+          mma_ss(d, FEW ? kd : qd, FEW ? qd : kd, S::kIdescQK, kk > 0 ? 1u : 0u);
+        }
         tc_commit(bSFull(c));
       }
       __syncwarp();
       return true;
     };
     auto issue_pv = [&](int c) -> bool {
-      if (!__all_sync(0xffffffffu, ctl.wait(bVFull(c), parV(c)) && ctl.wait(bPFull(c), parS(c)))) return false;
+      if (!__all_sync(0xffffffffu, ctl.wait(bVFull(c), parV(c)) && ctl.wait(bPFull(c), parK(c)))) return false;
       tc_fence_after();
-      const uint32_t pa = tmem + S::kColS + (c & 1) * kChunk;
+      const uint32_t pa = tmem + S::kColS + (c % kKS) * S::kSCols;
       const uint32_t vb = v_lo + uint32_t(c % kVS) * (S::kTileBytes >> 4);
-      if (leader) {
+      if constexpr (FEW) {
+        const uint32_t pb = p_lo + uint32_t(c % kKS) * (S::kPBytes >> 4);
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < kChunk / 16; ++kk)
+            mma_ss(tmem + S::kColO, desc_from(vb + kk * 16 * 128 / 16, kHiV),
+                   desc_from(pb + kk * 2 * S::kKeysP / 16, kHiP), S::kIdescPV, (c > 0 || kk > 0) ? 1u : 0u);
+          tc_commit(bODone(c));
+        }
+      } else if (leader) {
 #pragma unroll
         for (int part2 = 0; part2 < 2; ++part2)            // P's upper bits, then the rest of it
 #pragma unroll
@@ -492,6 +561,173 @@ __global__ void __launch_bounds__(kThreads, 2)
       wait_drain(bDrain, 0, kDrainNs);
     }
     __syncwarp();
+  } else if constexpr (FEW) {
+    // ================================================================ softmax, one key per thread
+    // Lanes 0-63 of S^T are the chunk's keys; all four warps hold O^T, a lane
+    // for each of d.  The two warps with keys exchange a bit a chunk, whether a
+    // row's max has to move, and its maxima only then.  What they exchange is
+    // kept twice, by the chunk's parity: chunk c + 2 is not in TMEM before
+    // every warp has passed chunk c.
+    const int q4 = warp & 3, key = q4 * 32 + lane;
+    const bool keyed = q4 < 2;
+    const uint32_t lane_base = tmem + (uint32_t(q4 * 32) << 16);
+    const float sl2 = p.scale_log2;
+    float* const s_max = reinterpret_cast<float*>(smem + S::kOffMax);
+    volatile int* const s_need = reinterpret_cast<volatile int*>(smem + S::kOffMax + 6 * kFew * 4);
+    float neg[kFew], l[kFew];                    // -m (0 while a row has no finite score), l
+    unsigned fresh = (1u << vr) - 1u;            // rows without a finite score so far
+    unsigned moved = 0;                          // parity of the exchanges of maxima, a bit for each parity of the chunk
+#pragma unroll
+    for (int x = 0; x < kFew; ++x) neg[x] = l[x] = 0.f;
+    bool ok = true;
+    for (int c = 0; c < nch; ++c) {
+      const int odd = c & 1;
+      float sv[kFew], pr[kFew];
+      const bool ends = r.c0 + c == r.last && r.tail < kChunk;
+      if (keyed) {
+        ok = __all_sync(0xffffffffu, ctl.wait(bSFull(c), parK(c)));
+        if (!ok) break;
+        tc_fence_after();
+        tmem_ld8(lane_base + S::kColS + (c % kKS) * S::kSCols, sv);
+        tmem_wait_ld();
+        const bool past = ends && key >= r.tail;
+        bool need = false;
+#pragma unroll
+        for (int x = 0; x < kFew; ++x) {
+          pr[x] = 0.f;
+          if (x >= vr) continue;
+          if (past) sv[x] = -INFINITY;
+          if constexpr (!TREE) p.scores[size_t(f0 + x) * p.score_stride + size_t(r.c0 + c) * kChunk + key] = sv[x];
+          pr[x] = fmaf(sv[x], sl2, neg[x]);
+          // the row moves its max only by more than 2^8; the first finite score always moves it
+          need |= pr[x] > (fresh >> x & 1u ? -INFINITY : kRescaleThreshold);
+        }
+        need = __any_sync(0xffffffffu, need);
+        if (lane == 0) {
+          s_need[odd * 2 + q4] = need;
+          mbar_arrive(bMax + 8u * odd);
+        }
+        // the product that read this P buffer last
+        if (c >= kKS) ok = __all_sync(0xffffffffu, ctl.wait(bODone(c - kKS), parV(c - kKS)));
+        if (!ok) break;
+#pragma unroll
+        for (int x = 0; x < kFew; ++x)
+          if (x < vr) pr[x] = ex2(pr[x]);
+      }
+      ok = __all_sync(0xffffffffu, ctl.wait(bMax + 8u * odd, uint32_t(c >> 1) & 1u));
+      if (!ok) break;
+      if (s_need[odd * 2] | s_need[odd * 2 + 1]) {     // the same in every thread
+        float* const mine = s_max + odd * 2 * kFew;
+        if (keyed) {
+          float top = -INFINITY;                 // lane x's own: row x's max in this warp
+#pragma unroll
+          for (int x = 0; x < kFew; ++x) {
+            if (x >= vr) continue;
+            const float v = warp_max(sv[x]);
+            if (lane == x) top = v;
+          }
+          if (lane < kFew) mine[q4 * kFew + lane] = top;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bTop + 8u * odd);
+        }
+        ok = __all_sync(0xffffffffu, ctl.wait(bTop + 8u * odd, moved >> odd & 1u));
+        if (!ok) break;
+        moved ^= 1u << odd;
+        float alpha[kFew];
+#pragma unroll
+        for (int x = 0; x < kFew; ++x) {
+          alpha[x] = 1.f;
+          if (x >= vr) continue;
+          const float mb = fmaxf(mine[x], mine[kFew + x]) * sl2;
+          const float old = fresh >> x & 1u ? -INFINITY : -neg[x];
+          if (mb > old + kRescaleThreshold) {
+            alpha[x] = ex2(old - mb);
+            neg[x] = -mb;
+            fresh &= ~(1u << x);
+          }
+          l[x] *= alpha[x];
+          if (keyed) pr[x] = ex2(fmaf(sv[x], sl2, neg[x]));
+        }
+        if (c > 0) {
+          ok = __all_sync(0xffffffffu, ctl.wait(bODone(c - 1), parV(c - 1)));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            float ov[kFew];
+            tmem_ld8(lane_base + S::kColO + half * kFew, ov);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < kFew; ++x) ov[x] *= alpha[x];
+            tmem_st8(lane_base + S::kColO + half * kFew, ov);
+          }
+          tmem_wait_st();
+        }
+      }
+      if (keyed) {
+        const uint32_t to = base + S::kOffP + (c % kKS) * S::kPBytes + (key >> 3) * S::kKeysP + (key & 7) * 16;
+        uint32_t hi[kFew / 2], lo[kFew / 2];
+#pragma unroll
+        for (int x = 0; x < kFew; x += 2) {
+          const uint32_t a = __float_as_uint(pr[x]), bb = __float_as_uint(pr[x + 1]);
+          hi[x / 2] = __byte_perm(a, bb, 0x7632);
+          lo[x / 2] = pack_bf16(rest_of(a, x < vr ? 1e-30f : 0.f), rest_of(bb, x + 1 < vr ? 1e-30f : 0.f));
+          l[x] += pr[x];
+          l[x + 1] += pr[x + 1];
+        }
+        st_shared_v4(to, hi[0], hi[1], hi[2], hi[3]);
+        st_shared_v4(to + 128, lo[0], lo[1], lo[2], lo[3]);
+        if (ends) {
+          // values behind the cached tokens, as below
+          ok = __all_sync(0xffffffffu, ctl.wait(bVFull(c), parV(c)));
+          if (!ok) break;
+          const uint32_t v0 = sV + (c % kVS) * S::kTileBytes;
+          const int total = (kChunk - r.tail) * (HD / 8);
+          for (int x = key; x < total; x += 64) {
+            const int at = r.tail + x / (HD / 8), piece = x % (HD / 8);
+            st_shared_v4(v0 + (piece >> 3) * S::kAtomKV + at * 128 + (piece & 7) * 16, 0u, 0u, 0u, 0u);
+          }
+        }
+        fence_proxy_async();
+      }
+      tc_fence_before();
+      mbar_arrive(bPFull(c));
+    }
+    if (ok) ok = __all_sync(0xffffffffu, ctl.wait(bODone(nch - 1), parV(nch - 1)));
+    if (ok) {
+      tc_fence_after();
+      float hi[kFew], lo[kFew];
+      tmem_ld8(lane_base + S::kColO, hi);
+      tmem_ld8(lane_base + S::kColO + kFew, lo);
+      tmem_wait_ld();
+      if (key < HD) {
+#pragma unroll
+        for (int x = 0; x < kFew; ++x)
+          if (x < vr) p.part_o[(part + x) * HD + key] = hi[x] + lo[x];
+      }
+      // the rows' sums over the two warps with keys
+      float* const s_sum = s_max + 4 * kFew;
+      if (keyed) {
+        float mine = 0.f;
+#pragma unroll
+        for (int x = 0; x < kFew; ++x) {
+          float v = l[x];
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+          if (lane == x) mine = v;
+        }
+        if (lane < kFew) s_sum[q4 * kFew + lane] = mine;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bSum);
+      }
+      if (q4 == 0 && __all_sync(0xffffffffu, ctl.wait(bSum, 0))) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < kFew; ++x)
+          if (lane == x && !(fresh >> x & 1u)) top = -neg[x];
+        if (lane < vr) p.part_ml[part + lane] = make_float2(top, s_sum[lane] + s_sum[kFew + lane]);
+      }
+    }
   } else if ((warp & 3) < warps) {
     // ================================================================ softmax, one row per thread
     const int q4 = warp & 3;
@@ -500,17 +736,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t lane_base = tmem + (uint32_t(q4 * 32) << 16);
     const float sl2 = p.scale_log2;
     // A row that the tile only has room for gets P = 0, not the 1 of its zero
-    // scores: a step's tile has 30 of them for 2 rows, and the tensor cores'
-    // power lowers the clocks (16 x 16K steps for seconds: 181 us each for 184).
+    // scores, which would cost the tensor cores power.
     const float least = mine ? 1e-30f : 0.f;
     float m2 = -INFINITY, l = 0.f;
     bool ok = true;
     for (int c = 0; c < nch; ++c) {
-      ok = __all_sync(0xffffffffu, ctl.wait(bSFull(c), parS(c)));
+      ok = __all_sync(0xffffffffu, ctl.wait(bSFull(c), parK(c)));
       if (!ok) break;
       tc_fence_after();
       float sv[kChunk];
-      const uint32_t s_col = lane_base + S::kColS + (c & 1) * kChunk;
+      const uint32_t s_col = lane_base + S::kColS + (c % kKS) * kChunk;
       tmem_ld32(s_col, sv);
       tmem_ld32(s_col + 32, sv + 32);
       tmem_wait_ld();
@@ -1005,10 +1240,10 @@ struct Call {
   cudaStream_t stream;
 };
 
-template <int BLK, int HD, bool TREE>
-int launch(const Call& c, const Params& p) {
-  using S = Shape<BLK, HD>;
-  auto kern = paged_attention_kernel<BLK, HD, TREE>;
+template <int BLK, int HD, bool TREE, bool FEW>
+int launch_rows(const Call& c, const Params& p) {
+  using S = Shape<BLK, HD, FEW>;
+  auto kern = paged_attention_kernel<BLK, HD, TREE, FEW>;
   // enough shared memory that no third CTA shares an SM: TMEM holds two
   constexpr int smem = S::kSmem < 77 * 1024 ? 77 * 1024 : S::kSmem;
   static_assert(2 * (smem + 1024) <= 228 * 1024, "two CTAs per SM");
@@ -1026,7 +1261,7 @@ int launch(const Call& c, const Params& p) {
     }
   }
   CUtensorMap mq, mk, mv;
-  int st = tmap::encode_rows(&mq, c.q, c.batch * c.plan.hg, c.plan.rows, HD, kTileM);
+  int st = tmap::encode_atoms(&mq, c.q, c.batch * c.plan.hg, c.plan.rows, HD, S::kRowsQ);
   if (st == BSA_OK) st = tmap::encode_rows(&mk, c.k_cache, p.num_pages * p.hkv, BLK, HD, kChunk);
   if (st == BSA_OK) st = tmap::encode_rows(&mv, c.v_cache, p.num_pages * p.hkv, BLK, HD, kChunk);
   if (st != BSA_OK) return st;
@@ -1043,6 +1278,11 @@ int launch(const Call& c, const Params& p) {
     return launch_dependent("step join launch", join_step_kernel<BLK, HD>, grid, kJoinWarps * 32, 0, 1, c.stream, p,
                             c.heads, row_blocks);
   }
+}
+
+template <int BLK, int HD, bool TREE>
+int launch(const Call& c, const Params& p) {
+  return p.rows <= kFew ? launch_rows<BLK, HD, TREE, true>(c, p) : launch_rows<BLK, HD, TREE, false>(c, p);
 }
 
 bool aligned(const void* x, uintptr_t a) { return (reinterpret_cast<uintptr_t>(x) % a) == 0; }

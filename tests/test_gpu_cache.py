@@ -286,6 +286,43 @@ def test_step_weights(case):
     lay.close()
 
 
+@pytest.mark.parametrize("H,G,d,B", [(16, 16, 64, 64), (48, 16, 64, 128), (128, 16, 64, 64), (64, 8, 128, 64), (128, 8, 64, 64)])
+@pytest.mark.parametrize("late", [False, True])
+def test_step_whose_maxima_keep_moving(H, G, d, B, late):
+    """1 to 16 query heads a key/value head over runs of several chunks: scores that rise by 10 from chunk to chunk
+    (even heads) or fall (odd heads), and, `late`, no finite score in the first 192 tokens."""
+    n, batch = 1000, 128 // G
+    lay = _layout(OL.BAND_GLOBAL, n, B, 1, dict(window=-(-n // B), global_first=0))
+    sets = OL.kept_sets(OL.BAND_GLOBAL, n, B, 1, window=-(-n // B), global_first=0)
+    kc, vc, table, th = _paged(batch, G, n, B, d, 50)
+    at = [n - 1 - 37 * b for b in range(batch)]
+    token = torch.arange(-(-n // B) * B, device="cuda").view(-1, B)
+    for b in range(batch):
+        pages = table[b].long()
+        kc[pages] *= 0.25
+        kc[pages, :, :, 0] = (token // 64 * 10).to(torch.bfloat16)[:, None]
+        if late:
+            kc[pages, :, :, 1] = torch.where(token < 192, float("-inf"), 0.5).to(torch.bfloat16)[:, None]
+    _blank(kc, vc, th, B, [t + 1 for t in at])
+    q = to_device_bf16(inputs.normal_bf16_bits((batch * H, d), 51)) * 0.25
+    q[:, 0] = torch.where(torch.arange(batch * H, device="cuda") % 2 == 0, 1.0, -1.0)
+    q[:, 1] = 0.5
+    w = torch.zeros((batch * G, n), device="cuda")
+    o, lse = bsa.decode_weights(q, kc, vc, table, torch.tensor(at, dtype=torch.int32, device="cuda"), lay, batch, w, 1.0)
+    torch.cuda.synchronize()
+    bsa.bsa_get_status(lay.handle)
+    qh, kh, vh = _np(q), np.nan_to_num(_np(kc), neginf=-np.inf), np.nan_to_num(_np(vc))
+    o_ref, lse_ref = OD.decode_step(qh, kh, vh, th, at, sets, B, 1.0)
+    e_p = _e_p(1.0, d, qh, np.where(np.isinf(kh), 0, kh), lse_ref)
+    _close_lse(_np(lse), lse_ref, e_p)
+    _close_o(_np(o), o_ref, e_p, vh)
+    want = OC.step_weights(qh, kh, th, at, lse_ref, sets, B, 1.0, n)
+    bound = want * (2 * e_p + 2.0 ** -21 + (H // G) * 2.0 ** -24) + 1e-30
+    assert np.all(np.abs(_np(w) - want) <= bound), (np.abs(_np(w) - want) / bound).max()
+    assert e_p < 5e-3 and (not late or (want[:, :192] == 0).all())
+    lay.close()
+
+
 def test_step_agrees_with_decode_and_long_rows_split():
     n, B, batch, H, G, d = 32768, 64, 2, 4, 2, 128
     lay = _layout(OL.BAND_GLOBAL, n, B, 1, dict(window=n // B, global_first=0))
