@@ -264,6 +264,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
     prefix |= uint32_t(s_digit) << shift;
     mask |= dm << shift;
     left = s_left;
+    if (s_equal == left) break;          // all keys under the prefix stay: its lower bits do not matter
   }
   const bool split = s_equal > left;     // some keys equal to the last one stay, some go
   // keys above `prefix` are kept, and of those equal to it the first `left`

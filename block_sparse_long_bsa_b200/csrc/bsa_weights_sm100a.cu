@@ -421,9 +421,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bSFree0 + 8u * (tt % kSBufs));
           }
-          if (dead || blk == diag) {
-            // the diagonal block takes queries from the key's own token on; a
-            // query row without weight gives nothing, whatever its scores are
+          // In the diagonal block a key takes queries from its own token on: of
+          // these 32 all, none, or (where they are the warp's own tokens) some.
+          const int first = blk == diag ? kl - lane : -32;
+          if (c0 % BLK < first) {
+          } else if (dead || c0 % BLK == first) {
+            // a query row without weight gives nothing, whatever its scores are
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
               const float n = neg[c0 + c];
