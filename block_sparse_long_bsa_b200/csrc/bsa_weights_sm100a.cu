@@ -463,10 +463,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // for each: four slices of the column's rows, four keys a thread.  A column of
 // more than kLong rows (a global first block's) is shared out over the whole
 // block instead.  What this costs is the latency of its loads, so those of the
-// layout are made before the wait for the first kernel, and those of the sums
+// layout and the weights so far are made before the wait for the first kernel, and those of the sums
 // four at a time: 23.4 us a call at 2500 random tokens against 25.0 with eight,
 // and 29.3 with a thread to every key and one slice.
-constexpr int kAddThreads = 1024, kLong = 128, kStaged = 4096, kUnits = 8, kInFlight = 4;
+constexpr int kAddThreads = 1024, kLong = 64, kStaged = 4096, kUnits = 8, kInFlight = 4;
 template <int BLK>
 __global__ void __launch_bounds__(kAddThreads) add_rows_kernel(const Params p) {
   constexpr int SL = kAddThreads / BLK, RL = kAddThreads / (BLK / 4);
@@ -480,6 +480,8 @@ __global__ void __launch_bounds__(kAddThreads) add_rows_kernel(const Params p) {
   const int u = (j0 + sl) * BLK + kl;
   float* const f = reinterpret_cast<float*>(s_sum);
   grid_release();
+  float* const out = p.weights + size_t(p.kv0 + kvl) * p.weights_stride + u;
+  const float old = u < p.n ? *out : 0.f;
   float4 t4 = make_float4(0.f, 0.f, 0.f, 0.f);   // this thread's slice of column sl
   float sum = 0.f;                               // of key kl of a long column sl
 #pragma unroll 1
@@ -563,7 +565,7 @@ __global__ void __launch_bounds__(kAddThreads) add_rows_kernel(const Params p) {
   // a wait that ran out left sums unwritten: nothing is added then
   if (u >= p.n || (*reinterpret_cast<volatile uint32_t*>(p.status) & kStatusTimeout)) return;
   const float* const mine = f + sl * 4 * BLK + kl;
-  p.weights[size_t(p.kv0 + kvl) * p.weights_stride + u] += ((mine[0] + mine[BLK]) + (mine[2 * BLK] + mine[3 * BLK])) + sum;
+  *out = old + (((mine[0] + mine[BLK]) + (mine[2 * BLK] + mine[3 * BLK])) + sum);
 }
 
 // Query heads of a unit: two for B = 64 when a group's heads pair off on one route.
