@@ -43,7 +43,8 @@
 //
 // Roles of kernel 1 (192 threads, two CTAs per SM): warp 0 looks the pages up
 // and issues the TMA loads, warp 1 issues the products, warps 2-5 hold one
-// query row per thread.  Every wait is bounded, as in the forward.
+// query row per thread (few rows: two of them one key per thread, all four a
+// lane of O^T).  Every wait is bounded, as in the forward.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -177,6 +178,7 @@ struct Shape {
   static constexpr uint32_t kIdescQK = idesc_bf16(kTileM, kSCols, 0, 0);
   static constexpr uint32_t kIdescPV = FEW ? idesc_bf16(kTileM, 2 * kFew, 1, 1) : idesc_bf16(kTileM, HD, 0, 1);
   static_assert(kColO + (FEW ? 2 * kFew : HD) <= int(kTmemCols), "TMEM budget");
+  static_assert(!FEW || kKS == kVS, "P buffers and V slots are released by the same products");
   static_assert(kOffBar % 8 == 0 && kOffP % 16 == 0, "alignment");
   // Few rows: a product of 128 rows reads 8 KB past a 64-row operand (the next slot, or what follows the last)
   static_assert(!FEW || kOffV + kVS * kTileBytes + kAtomKV <= 77 * 1024 || HD == 128, "inside the CTA's shared memory");
