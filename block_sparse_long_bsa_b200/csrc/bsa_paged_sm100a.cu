@@ -23,7 +23,7 @@
 // leaves its unnormalised O, m and l in the caller's workspace; the step
 // leaves the scores too.
 // Kernel 2 joins the runs of each row.  The tree's rows add their ancestors
-// there, at most T keys each, on the plain cores in fp32: an ancestor's key
+// there (before its wait for kernel 1, as far as its blocks find room beside that), at most T keys each, on the plain cores in fp32: an ancestor's key
 // and value are read by the rows that descend from it and by no others, so a
 // branch's infinity cannot reach another branch.  The step's kernel 2 also
 // turns the scores into weights, p = exp2(s scale log2 e - M) / L.
@@ -1143,7 +1143,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) join_tree_kernel(const Par
   // scores of the ancestors: 8 lanes a key, four keys at a time
   const int sub = lane >> 3, pc = lane & 7;
   const int kvh = b * p.hkv + hh / (p.H / p.hkv);
-  float top = -INFINITY;
+  float top = -INFINITY, sum = 0.f, anc[DPL] = {};   // the ancestors' part, under its own max
   if (live && !bad) {
     float qr[CPL];
     const uint4* qs = reinterpret_cast<const uint4*>(p.q + (size_t(f) * p.T + i) * HD + pc * CPL);
@@ -1183,8 +1183,32 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) join_tree_kernel(const Par
     }
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+    __syncwarp();
+    for (int x = lane; x < count; x += 32) {
+      const float s = s_sc[warp][x];
+      // one that is not read gets 0 and, as 0 times its value may be NaN, is left out below
+      const bool use = keeps >> ((len + count - 1 - x) / BLK - blk0) & 1u;
+      const float w = use ? ex2(s - (top == -INFINITY ? 0.f : top)) : 0.f;
+      s_sc[warp][x] = w;
+      sum += w;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    __syncwarp();
+#pragma unroll 4
+    for (int x = 0; x < count; ++x) {
+      if (!(keeps >> ((len + count - 1 - x) / BLK - blk0) & 1u)) continue;
+      const float w = s_sc[warp][x];
+      const uint32_t* vs = reinterpret_cast<const uint32_t*>(p.v_tree + (size_t(kvh) * p.T + s_path[warp][x]) * HD + lane * DPL);
+#pragma unroll
+      for (int e = 0; e < DPL; e += 2) {
+        float v0, v1;
+        bf16x2_to_f32(vs[e / 2], v0, v1);
+        anc[e] = fmaf(w, v0, anc[e]);
+        anc[e + 1] = fmaf(w, v1, anc[e + 1]);
+      }
+    }
   }
-  __syncwarp();
   grid_wait();                                    // the runs of kernel 1 are in memory from here on
   if (!live) return;
   float M = -INFINITY, L = 0.f, acc[DPL] = {};
@@ -1196,36 +1220,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) join_tree_kernel(const Par
     // the cache's part and the path's under one max
     const float all = fmaxf(M, top);
     const float a = M == -INFINITY ? (L == 0.f ? 0.f : 1.f) : ex2(M - all);
-    L *= a;
+    const float c = top == -INFINITY ? 1.f : ex2(top - all);
+    L = fmaf(L, a, sum * c);
 #pragma unroll
-    for (int e = 0; e < DPL; ++e) acc[e] *= a;
-    float sum = 0.f;
-    for (int x = lane; x < count; x += 32) {
-      const float s = s_sc[warp][x];
-      // one that is not read gets 0 and, as 0 times its value may be NaN, is left out below
-      const bool use = keeps >> ((len + count - 1 - x) / BLK - blk0) & 1u;
-      const float w = use ? ex2(s - (all == -INFINITY ? 0.f : all)) : 0.f;
-      s_sc[warp][x] = w;
-      sum += w;
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    L += sum;
+    for (int e = 0; e < DPL; ++e) acc[e] = fmaf(acc[e], a, anc[e] * c);
     M = all;
-    __syncwarp();
-#pragma unroll 4
-    for (int x = 0; x < count; ++x) {
-      if (!(keeps >> ((len + count - 1 - x) / BLK - blk0) & 1u)) continue;
-      const float w = s_sc[warp][x];
-      const uint32_t* vs = reinterpret_cast<const uint32_t*>(p.v_tree + (size_t(kvh) * p.T + s_path[warp][x]) * HD + lane * DPL);
-#pragma unroll
-      for (int e = 0; e < DPL; e += 2) {
-        float v0, v1;
-        bf16x2_to_f32(vs[e / 2], v0, v1);
-        acc[e] = fmaf(w, v0, acc[e]);
-        acc[e + 1] = fmaf(w, v1, acc[e + 1]);
-      }
-    }
   }
   store_row<HD>(p, size_t(f) * p.T + i, bad || flag, M, L, acc);
   if (lane == 0 && (bad || (flag & 1))) atomicOr(p.status, kStatusBadIndex);
