@@ -159,13 +159,20 @@ def _ptr(x) -> int:
     return x.data_ptr()
 
 
+_raw_stream = None            # torch's functions for the current stream's handle, once it runs CUDA
+
+
 def _stream(s) -> int:
+    global _raw_stream
     if s is None:
+        if _raw_stream is not None:
+            # the handle alone: building a Stream object takes several times as long
+            return _raw_stream[0](_raw_stream[1]())
         try:
             import torch
             if torch.cuda.is_initialized():
-                # the handle alone: building a Stream object takes several times as long
-                return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+                _raw_stream = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+                return _raw_stream[0](_raw_stream[1]())
             if torch.cuda.is_available():
                 return torch.cuda.current_stream().cuda_stream
         except ImportError:
