@@ -16,7 +16,8 @@
 // cluster); ties at it go to the lowest slots; ranks of holes and movers come
 // from ballots and scans over warps and blocks.
 // Kernel 2 (move_kernel), a warp per 32 slots: new weights, tokens and
-// lengths, and the moved rows, 16 bytes a lane.  Its bound is memory: 4 d
+// lengths, and the moved rows, 16 bytes a lane.  Small cuts have this done by
+// kernel 1's block instead.  Its bound is memory: 4 d
 // bytes read and written a moved token.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -99,6 +100,64 @@ __device__ __forceinline__ void add_peer(uint32_t a, int v) {
   asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 
+// Slot s of a row after the cut (a thread each, warps whole): its weight and
+// token, and the row that moves into it.  m: kept, newest token, -, 1 if nothing moves.
+template <int HD>
+__device__ __forceinline__ void move_slot(const Params& p, int row, int s, int4 m) {
+  constexpr int LPR = HD / 8;            // lanes of a row, 16 bytes each
+  constexpr int SPI = 32 / (2 * LPR);    // tokens a warp moves at once (key and value)
+  const int b = row / p.hkv, hk = row - b * p.hkv;
+  const int lane = threadIdx.x & 31;
+  const size_t at = size_t(row) * p.stride;
+  int from = s;
+  if (s < p.n) {
+    float wt = 0.f;
+    int t = int(int64_t(m.y) + 1 + (s - m.x));               // a slot behind takes the next token to come
+    if (s < m.x) {
+      if (!m.w) from = p.src[size_t(row) * p.cap + s];
+      if (from < 0) from = p.movers[size_t(row) * p.cap + (-1 - from)];
+      wt = p.weights[at + from];
+      t = p.tokens ? p.tokens[at + from] : from;
+    }
+    p.weights_out[at + s] = wt;
+    p.tokens_out[at + s] = t;
+  }
+  unsigned todo = __ballot_sync(0xffffffffu, from != s);
+  if (!todo) return;
+  // rows of the caches, counted in d-element rows (64-bit: long caches pass 2^31 elements)
+  int64_t to_row = 0, from_row = 0;
+  if (from != s) {
+    const int32_t* pt = p.page_table + size_t(b) * p.max_blocks;
+    to_row = (int64_t(pt[s / p.B]) * p.hkv + hk) * p.B + s % p.B;
+    from_row = (int64_t(pt[from / p.B]) * p.hkv + hk) * p.B + from % p.B;
+  }
+  const int sub = lane / (2 * LPR), in = lane % (2 * LPR);
+  uint4* const base = reinterpret_cast<uint4*>(in < LPR ? p.kc : p.vc) + in % LPR;
+  while (todo) {
+    constexpr int U = 4;                 // tokens in flight, times SPI
+    uint4 v[U];
+    int64_t dst[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // SPI tokens of the ballot: one for each part of the warp
+      int x = -1;
+#pragma unroll
+      for (int y = 0; y < SPI; ++y) {
+        const int first = todo ? __ffs(todo) - 1 : -1;
+        if (todo) todo &= todo - 1;
+        if (y == sub) x = first;
+      }
+      const int64_t f = __shfl_sync(0xffffffffu, from_row, x & 31);
+      dst[u] = __shfl_sync(0xffffffffu, to_row, x & 31);
+      if (x < 0) dst[u] = -1;
+      else v[u] = base[f * LPR];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (dst[u] >= 0) base[dst[u] * LPR] = v[u];
+  }
+}
+
 // A cluster of C blocks per row; block r owns the slots [r per, (r + 1) per).
 // Each block adds the bins that it has keys in (few: the keys under one prefix
 // share their upper bits) to every block's sum of histograms; the newest
@@ -106,6 +165,8 @@ __device__ __forceinline__ void add_peer(uint32_t a, int v) {
 // memory after a barrier.  Nothing read so is written again.  The loops are not
 // unrolled: a block runs through them once or a few times, and fetching their
 // instructions is what it would wait for.
+// HD > 0: the blocks go on to move the rows, and no second kernel runs.
+template <int HD>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int C) {
   extern __shared__ uint32_t s_keys[];
   __shared__ __align__(16) int hist[kBins];       // this block's
@@ -130,8 +191,19 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
   const int32_t* tok = p.tokens ? p.tokens + size_t(row) * p.stride : nullptr;
   auto refuse = [&]() {
     if (tid == 0 && rank == 0) {
-      p.meta[row] = make_int4(0, 0, 1, 1);
+      if (HD == 0) p.meta[row] = make_int4(0, 0, 1, 1);
+      else if (row % p.hkv == 0) p.lengths_out[b] = -1;
       atomicOr(p.status, kStatusBadIndex);
+    }
+  };
+  // the end of a row that is not refused
+  auto finish = [&](int4 m) {
+    if constexpr (HD > 0) {
+      if (tid == 0 && rank == 0 && row % p.hkv == 0) p.lengths_out[b] = m.x;
+#pragma unroll 1
+      for (int s0 = rank * kSelThreads; s0 < p.n; s0 += C * kSelThreads) move_slot<HD>(p, row, s0 + tid, m);
+    } else if (tid == 0 && rank == 0) {
+      p.meta[row] = m;
     }
   };
   if (len < 0 || len > p.n) {
@@ -170,8 +242,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
     if (len == 0) newest = -1;
   }
   if (len <= p.budget) {
-    if (tid == 0 && rank == 0) p.meta[row] = make_int4(len, newest, 0, 1);
     cluster_sync();                      // the others may still be reading s_newest here
+    finish(make_int4(len, newest, 0, 1));
     return;
   }
   const int64_t floor_tok = int64_t(newest) - p.recent;      // tokens above it are protected
@@ -337,18 +409,15 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
     mover0 += __popc(mb);
     hole0 += __popc(hb);
   }
-  if (tid == 0 && rank == 0) p.meta[row] = make_int4(p.budget, newest, 0, 0);
   cluster_wait();                        // no block ends while another may still read its shared memory
+  if (HD > 0) cluster_sync();            // all blocks' lists are written
+  finish(make_int4(p.budget, newest, 0, 0));
 }
 
 template <int HD>
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const Params p, int tiles) {
-  constexpr int LPR = HD / 8;            // lanes of a row, 16 bytes each
-  constexpr int SPI = 32 / (2 * LPR);    // tokens a warp moves at once (key and value)
   const int row = blockIdx.x / tiles, tile = blockIdx.x - row * tiles;
   const int b = row / p.hkv, hk = row - b * p.hkv;
-  const int lane = threadIdx.x & 31;
-  const int s = tile * kMoveThreads + threadIdx.x;
   // (no early start for the kernel after this one: the next cut's blocks took
   // room from the moves, 47 us a call against 49)
   grid_wait();
@@ -358,54 +427,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const Params p, int 
     return;
   }
   if (tile == 0 && threadIdx.x == 0 && hk == 0) p.lengths_out[b] = m.x;
-  const size_t at = size_t(row) * p.stride;
-  int from = s;
-  if (s < p.n) {
-    float wt = 0.f;
-    int t = int(int64_t(m.y) + 1 + (s - m.x));               // a slot behind takes the next token to come
-    if (s < m.x) {
-      if (!m.w) from = p.src[size_t(row) * p.cap + s];
-      if (from < 0) from = p.movers[size_t(row) * p.cap + (-1 - from)];
-      wt = p.weights[at + from];
-      t = p.tokens ? p.tokens[at + from] : from;
-    }
-    p.weights_out[at + s] = wt;
-    p.tokens_out[at + s] = t;
-  }
-  unsigned todo = __ballot_sync(0xffffffffu, from != s);
-  if (!todo) return;
-  // rows of the caches, counted in d-element rows (64-bit: long caches pass 2^31 elements)
-  int64_t to_row = 0, from_row = 0;
-  if (from != s) {
-    const int32_t* pt = p.page_table + size_t(b) * p.max_blocks;
-    to_row = (int64_t(pt[s / p.B]) * p.hkv + hk) * p.B + s % p.B;
-    from_row = (int64_t(pt[from / p.B]) * p.hkv + hk) * p.B + from % p.B;
-  }
-  const int sub = lane / (2 * LPR), in = lane % (2 * LPR);
-  uint4* const base = reinterpret_cast<uint4*>(in < LPR ? p.kc : p.vc) + in % LPR;
-  while (todo) {
-    constexpr int U = 4;                 // tokens in flight, times SPI
-    uint4 v[U];
-    int64_t dst[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      // SPI tokens of the ballot: one for each part of the warp
-      int x = -1;
-#pragma unroll
-      for (int y = 0; y < SPI; ++y) {
-        const int first = todo ? __ffs(todo) - 1 : -1;
-        if (todo) todo &= todo - 1;
-        if (y == sub) x = first;
-      }
-      const int64_t f = __shfl_sync(0xffffffffu, from_row, x & 31);
-      dst[u] = __shfl_sync(0xffffffffu, to_row, x & 31);
-      if (x < 0) dst[u] = -1;
-      else v[u] = base[f * LPR];
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (dst[u] >= 0) base[dst[u] * LPR] = v[u];
-  }
+  move_slot<HD>(p, row, tile * kMoveThreads + threadIdx.x, m);
 }
 
 bool aligned(const void* x, uintptr_t a) { return (reinterpret_cast<uintptr_t>(x) % a) == 0; }
@@ -439,7 +461,8 @@ int launch(const Params& p, int rows, int d, cudaStream_t stream) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev]) {
-      e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysInSmem * 4);
+      for (auto kern : {select_kernel<0>, select_kernel<64>, select_kernel<128>})
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysInSmem * 4);
       if (e != cudaSuccess) return set_error(BSA_ERR_CUDA, std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e));
       done[dev] = true;
     }
@@ -449,9 +472,17 @@ int launch(const Params& p, int rows, int d, cudaStream_t stream) {
   int C = 1;
   while (C < kMaxCluster && p.n > C * kSlotsPerBlock && rows * C <= 148) C *= 2;
   const int per = (p.n + C * 32 - 1) / (C * 32) * 32;
-  int st = launch_dependent("eviction select launch", select_kernel, unsigned(rows) * unsigned(C), kSelThreads,
+  // One kernel where a row has one block and few slots or moves, at most
+  // min(budget, n - budget): a launch less on the host.  (us, two kernels and
+  // one: 8 rows of 1000 slots cut to 500 13.7 and 11.7, 256 of them 22.1 and
+  // 20.8; 256 rows of 4000 cut to 3900 20.5 and 16.9; but to 3700 22.4 and 24.1,
+  // 8 of 2000 cut to 1000 13.5 and 15.9, 16 of 32768 cut to 8192 42.5 and 46.6:
+  // a row's own block takes its slots 512 at a time.)
+  const bool alone = C == 1 && (p.n <= 2 * kSelThreads || std::min(p.budget, p.n - p.budget) <= kSelThreads / 4);
+  const auto select = !alone ? select_kernel<0> : d == 128 ? select_kernel<128> : select_kernel<64>;
+  int st = launch_dependent("eviction select launch", select, unsigned(rows) * unsigned(C), kSelThreads,
                             size_t(std::min(per, kKeysInSmem)) * 4, unsigned(C), stream, p, C);
-  if (st != BSA_OK) return st;
+  if (st != BSA_OK || alone) return st;
   const int tiles = (p.n + kMoveThreads - 1) / kMoveThreads;
   const unsigned grid = unsigned(rows) * unsigned(tiles);
   return d == 128 ? launch_dependent("eviction move launch", move_kernel<128>, grid, kMoveThreads, 0, 1, stream, p, tiles)

@@ -362,7 +362,7 @@ size_t bsa_evict_workspace_bytes(const bsa_layout* layout, int batch, int kv_hea
  * outside [0, num_pages) among a sequence's cached tokens when it has to be
  * cut, leaves that sequence's caches, weights_out and tokens_out as they were,
  * sets lengths_out[b] = -1, and bsa_get_status then reports BSA_ERR_SHAPE.
- * Enqueues two kernels and returns; no allocation. */
+ * Enqueues one kernel (few slots or moves) or two and returns; no allocation. */
 int bsa_evict(void* k_cache, void* v_cache, const int32_t* page_table, int max_blocks,
               int num_pages, const int32_t* lengths, const float* weights,
               const int32_t* tokens, const bsa_layout* layout, int batch, int kv_heads, int d,

@@ -385,6 +385,10 @@ EVICT = [
     (64, 64, 1, 1, 64, 100, 3, [64], False),                # a budget past the cache: nothing to cut
     (70000, 128, 1, 1, 64, 30001, 500, [69999], True),      # a cluster of blocks for each row
     (400000, 128, 1, 1, 64, 100001, 500, [399999], True),   # longer than the keys that their shared memory holds
+    (1024, 128, 2, 2, 64, 512, 64, [1024, 700], False),     # few slots: one kernel
+    (1025, 64, 2, 2, 128, 512, 64, [1025, 513], True),      # two
+    (3000, 64, 3, 2, 128, 2950, 100, [3000, 2960, 10], True),   # few moves: one
+    (4096, 64, 2, 2, 64, 1500, 0, [4096, 1501], False),     # two
 ]
 
 
