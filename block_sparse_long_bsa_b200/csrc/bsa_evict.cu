@@ -35,6 +35,11 @@ namespace evict {
 
 using ptx::grid_release;
 using ptx::grid_wait;
+using ptx::cluster_arrive;
+using ptx::cluster_sync;
+using ptx::cluster_wait;
+using ptx::ld_peer;
+using ptx::peer_addr;
 
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 4 * kSelThreads;          // of an 11-bit digit, four a thread
@@ -73,28 +78,6 @@ __device__ __forceinline__ int cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return int(r);
-}
-// All threads of all blocks of the cluster; shared memory written before it is
-// seen by the others after it.
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_sync() {
-  cluster_arrive();
-  cluster_wait();
-}
-__device__ __forceinline__ uint32_t peer_addr(const void* p, int rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-               : "=r"(a)
-               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
-  return a;
-}
-__device__ __forceinline__ int ld_peer(uint32_t a) {
-  int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
 }
 __device__ __forceinline__ void add_peer(uint32_t a, int v) {
   asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(a), "r"(v) : "memory");

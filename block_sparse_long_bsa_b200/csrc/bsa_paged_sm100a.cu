@@ -26,7 +26,8 @@
 // there (before its wait for kernel 1, as far as its blocks find room beside that), at most T keys each, on the plain cores in fp32: an ancestor's key
 // and value are read by the rows that descend from it and by no others, so a
 // branch's infinity cannot reach another branch.  The step's kernel 2 also
-// turns the scores into weights, p = exp2(s scale log2 e - M) / L.
+// turns the scores into weights, p = exp2(s scale log2 e - M) / L.  Short steps
+// have no kernel 2: their runs are a cluster's, which does this itself.
 //
 // At most 8 rows (every step of a grouped-query model, short trees) take the
 // products the other way round, keys as the rows of a tile:
@@ -80,6 +81,13 @@ constexpr uint64_t kWaitNs = 1000000000ull, kDrainNs = 200000000ull;
 // longer than kRunChunks, so that sequences of other lengths level out (16 x 16K
 // step: 2 runs of 128 chunks 176 us, 4 of 64 169, 8 of 32 176).
 constexpr int kSlots = 2 * 148;
+// A step of at most 8 query rows a unit and few chunks is one kernel, a
+// cluster of up to 8 CTAs per unit that joins its runs through shared memory:
+// a launch less.  (A step of the dyadic route at 32K 11.1 us for 13.1 through
+// the binding, 8.0 for 8.8 in a graph; whole caches of 2000 tokens, the most
+// chunks there are, 11.0 for 13.1 and 9.5 for 10.9; four sequences 11.5 for 13.1
+// and 11.1 for 12.4.)
+constexpr int kAloneChunks = 4;        // chunks of a run at most
 constexpr int kRunChunks = 64;
 
 struct Plan {
@@ -91,9 +99,10 @@ struct Plan {
   int units;       // batch * hg * mtiles * groups
   int S;           // runs of a unit
   int cap;         // rows of a partial result
+  bool alone;      // one kernel, S CTAs of a cluster a unit
 };
 
-Plan plan_of(const bsa_layout* L, int batch, int heads, int kv_heads, int T) {
+Plan plan_of(const bsa_layout* L, int batch, int heads, int kv_heads, int T, bool step) {
   Plan p{};
   const int H = heads / batch, hkv = kv_heads / batch;
   p.hpt = L->L == 1 ? H / hkv : 1;
@@ -107,6 +116,15 @@ Plan plan_of(const bsa_layout* L, int batch, int heads, int kv_heads, int T) {
   const int fill = int(std::min<int64_t>(chunks, std::max<int64_t>(1, kSlots / busy)));
   p.S = std::max(fill, (chunks + kRunChunks - 1) / kRunChunks);
   p.cap = std::min(kTileM, p.rows);
+  // (a key/value head's query heads are one unit, so that one thread adds a key's weight)
+  if (step && p.rows <= kFew && (L->L == 1 || H == hkv)) {
+    int C = 8;
+    while (C > chunks) C /= 2;
+    if (chunks <= C * kAloneChunks && busy * C <= kSlots) {
+      p.alone = true;
+      p.S = C;
+    }
+  }
   return p;
 }
 
@@ -255,6 +273,14 @@ struct Run {
   int go;          // 0: nothing to do and nothing will be read
 };
 
+// A short step's end: what the cluster's CTAs join.
+struct End {
+  float2 ml[kFew];         // read by the others, as is `state`
+  int state;
+  int flag[kFew];          // joined
+  float M[kFew], L[kFew], w[kFew][8];
+};
+
 // Depth of every drafted token by pointer jumping: after round k a token
 // points 2^k ancestors up.  A parent that is not an earlier token ends the
 // walk (kernel 2 refuses such a token).  Called by all threads.
@@ -295,7 +321,7 @@ __device__ __forceinline__ bool keeps_all(const Params& p, size_t at, int blocks
   return blocks == 0 || (p.row_ptr[at + 1] - start >= blocks && p.col_idx[start + blocks - 1] == blocks - 1);
 }
 
-template <int BLK, int HD, bool TREE, bool FEW>
+template <int BLK, int HD, bool TREE, bool FEW, bool ALONE>
 __global__ void __launch_bounds__(kThreads, 2)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV, const Params p) {
@@ -334,6 +360,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kOffMisc + 4);
   volatile int* s_flag = reinterpret_cast<volatile int*>(smem + S::kOffMisc + 8);
   Run* s_run = reinterpret_cast<Run*>(smem + S::kOffRun);
+  End* const s_end = reinterpret_cast<End*>(smem + S::kOffK);   // ALONE, once the products are done
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Ctl ctl{abort_flag, p.status, kWaitNs};
   if (threadIdx.x == 0) {
@@ -424,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const Run r = *s_run;
   const int nch = r.c1 - r.c0;
   const size_t part = (size_t(unit) * p.S + run) * p.cap;
-  if (nch <= 0) {
+  if (!ALONE && nch <= 0) {
     // an empty run: l = 0 tells kernel 2 that its O was not written
     if (r.go) {
       for (int x = threadIdx.x; x < vr; x += kThreads) p.part_ml[part + x] = make_float2(-INFINITY, 0.f);
@@ -434,7 +461,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     return;
   }
 
-  if (warp == 0) {
+  if (ALONE && nch <= 0) {
+  } else if (warp == 0) {
     // ================================================================ loads
     const bool leader = elect_one();
     if (leader) {
@@ -502,11 +530,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ================================================================ products
     const bool leader = elect_one();
     constexpr uint64_t kFixK = sw128_fixed(16, 1024), kFixV = sw128_fixed(S::kAtomKV, 1024);
-    const uint32_t q_lo = uint32_t(kFixK) + (sQ >> 4), k_lo = uint32_t(kFixK) + (sK >> 4);
-    const uint32_t v_lo = uint32_t(kFixV) + (sV >> 4);
+    // (in a cluster an address's upper bits name the CTA; a descriptor's has 18 bits)
+    auto field = [](uint32_t addr) { return (addr & 0x3FFFFu) >> 4; };
+    const uint32_t q_lo = uint32_t(kFixK) + field(sQ), k_lo = uint32_t(kFixK) + field(sK);
+    const uint32_t v_lo = uint32_t(kFixV) + field(sV);
     constexpr uint32_t kHiK = uint32_t(kFixK >> 32), kHiV = uint32_t(kFixV >> 32);
     constexpr uint64_t kFixP = flat_fixed(S::kKeysP, 128);
-    const uint32_t p_lo = uint32_t(kFixP) + ((base + S::kOffP) >> 4);
+    const uint32_t p_lo = uint32_t(kFixP) + field(base + S::kOffP);
     constexpr uint32_t kHiP = uint32_t(kFixP >> 32);
     auto issue_qk = [&](int c) -> bool {
       if (!__all_sync(0xffffffffu, ctl.wait(bKFull(c), parK(c)))) return false;
@@ -705,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (key < HD) {
 #pragma unroll
         for (int x = 0; x < kFew; ++x)
-          if (x < vr) p.part_o[(part + x) * HD + key] = hi[x] + lo[x];
+          if (x < vr) (ALONE ? reinterpret_cast<float*>(smem) + x * HD : p.part_o + (part + x) * HD)[key] = hi[x] + lo[x];
       }
       // the rows' sums over the two warps with keys
       float* const s_sum = s_max + 4 * kFew;
@@ -727,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int x = 0; x < kFew; ++x)
           if (lane == x && !(fresh >> x & 1u)) top = -neg[x];
-        if (lane < vr) p.part_ml[part + lane] = make_float2(top, s_sum[lane] + s_sum[kFew + lane]);
+        if (lane < vr) (ALONE ? s_end->ml : p.part_ml + part)[lane] = make_float2(top, s_sum[lane] + s_sum[kFew + lane]);
       }
     }
   } else if ((warp & 3) < warps) {
@@ -861,7 +891,90 @@ __global__ void __launch_bounds__(kThreads, 2)
     tmem_dealloc(tmem, S::kTmemCols);
   }
   // 1: a page was out of range, 2: a wait ran out (the partial result is not whole)
-  if (threadIdx.x == 0) p.part_flag[size_t(unit) * p.S + run] = *s_flag | (*abort_flag ? 2 : 0);
+  const int state = *s_flag | (*abort_flag ? 2 : 0);
+  if constexpr (!ALONE) {
+    if (threadIdx.x == 0) p.part_flag[size_t(unit) * p.S + run] = state;
+  } else {
+    // ================================================================ the step's end, by the unit's cluster
+    // Each CTA has its O in its query tile's place, and m and l behind it; a row's
+    // are joined by the CTA whose turn it is, and each CTA adds the weights of
+    // its own keys, a thread those whose scores it wrote.
+    const int tid = threadIdx.x;
+    if (tid == 0) s_end->state = state;
+    if (nch <= 0 && tid < kFew) s_end->ml[tid] = make_float2(-INFINITY, 0.f);
+    const int key = (warp & 3) * 32 + lane;
+    const bool keyed = warp >= 2 && key < kChunk;
+    int u[kAloneChunks];
+    float old[kAloneChunks];
+    float* const w = p.weights + size_t(b * p.hkv + (p.L == 1 ? hg : hg / (p.H / p.hkv))) * p.weights_stride;
+#pragma unroll
+    for (int c = 0; c < kAloneChunks; ++c) {
+      const int x = r.c0 + c;
+      u[c] = -1;
+      if (keyed && c < nch && !(x == r.last && key >= r.tail))
+        u[c] = p.col_idx[r.start + x / CPB] * BLK + x % CPB * kChunk + key;
+    }
+#pragma unroll
+    for (int c = 0; c < kAloneChunks; ++c) old[c] = u[c] >= 0 ? w[u[c]] : 0.f;
+    cluster_sync();
+    if (tid < kFew * 8) {                         // row tid / 8, run tid % 8
+      const int x = tid >> 3, peer = tid & 7;
+      float m = -INFINITY, l = 0.f;
+      int flag = 0;
+      if (peer < p.S && x < vr) {
+        m = ld_peer_f32(peer_addr(&s_end->ml[x].x, peer));
+        l = ld_peer_f32(peer_addr(&s_end->ml[x].y, peer));
+        flag = ld_peer(peer_addr(&s_end->state, peer));
+      }
+      float M = l != 0.f ? m : -INFINITY;
+#pragma unroll
+      for (int off = 4; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+      const float wt = l == 0.f ? 0.f : M == -INFINITY ? 1.f : ex2(m - M);
+      float L = wt * l;
+#pragma unroll
+      for (int off = 4; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+#pragma unroll
+      for (int off = 4; off > 0; off >>= 1) flag |= __shfl_xor_sync(0xffffffffu, flag, off);
+      s_end->w[x][peer] = wt;
+      if (peer == 0) {
+        s_end->M[x] = M;
+        s_end->L[x] = L;
+        s_end->flag[x] = flag;
+      }
+    }
+    __syncthreads();
+    const bool refuse = !r.go || s_end->flag[0];
+    if (tid < HD) {
+      for (int x = run; x < vr; x += p.S) {
+        float o = 0.f;
+        for (int peer = 0; peer < p.S; ++peer) {
+          const float wt = s_end->w[x][peer];
+          if (wt != 0.f) o = fmaf(wt, ld_peer_f32(peer_addr(reinterpret_cast<float*>(smem) + x * HD + tid, peer)), o);
+        }
+        const float L = s_end->L[x];
+        const bool none = refuse || L == 0.f;
+        p.o[size_t(f0 + x) * HD + tid] = __float2bfloat16_rn(none ? 0.f : o / L);
+        if (tid == 0) p.lse[f0 + x] = none ? -INFINITY : (s_end->M[x] + __log2f(L)) * kLn2;
+      }
+    }
+    if (tid == 0 && run == 0 && (!r.go || (s_end->flag[0] & 1))) atomicOr(p.status, kStatusBadIndex);
+    if (!refuse) {
+      float sum[kAloneChunks] = {};
+      for (int x = 0; x < vr; ++x) {
+        const float L = s_end->L[x], M = s_end->M[x];
+        if (L == 0.f) continue;                   // a row without any weight adds nothing
+        const float neg = M == -INFINITY ? 0.f : -M, inv = 1.f / L;
+        const float* const sc = p.scores + size_t(f0 + x) * p.score_stride + size_t(r.c0) * kChunk + key;
+#pragma unroll
+        for (int c = 0; c < kAloneChunks; ++c)
+          if (u[c] >= 0) sum[c] = fmaf(ex2(fmaf(sc[c * kChunk], p.scale_log2, neg)), inv, sum[c]);
+      }
+#pragma unroll
+      for (int c = 0; c < kAloneChunks; ++c)
+        if (u[c] >= 0) w[u[c]] = old[c] + sum[c];
+    }
+    cluster_sync();                               // no CTA ends while another may still read its shared memory
+  }
 }
 
 // ------------------------------------------------------------ kernel 2
@@ -1241,10 +1354,10 @@ struct Call {
   cudaStream_t stream;
 };
 
-template <int BLK, int HD, bool TREE, bool FEW>
+template <int BLK, int HD, bool TREE, bool FEW, bool ALONE>
 int launch_rows(const Call& c, const Params& p) {
   using S = Shape<BLK, HD, FEW>;
-  auto kern = paged_attention_kernel<BLK, HD, TREE, FEW>;
+  auto kern = paged_attention_kernel<BLK, HD, TREE, FEW, ALONE>;
   // enough shared memory that no third CTA shares an SM: TMEM holds two
   constexpr int smem = S::kSmem < 77 * 1024 ? 77 * 1024 : S::kSmem;
   static_assert(2 * (smem + 1024) <= 228 * 1024, "two CTAs per SM");
@@ -1266,9 +1379,9 @@ int launch_rows(const Call& c, const Params& p) {
   if (st == BSA_OK) st = tmap::encode_rows(&mk, c.k_cache, p.num_pages * p.hkv, BLK, HD, kChunk);
   if (st == BSA_OK) st = tmap::encode_rows(&mv, c.v_cache, p.num_pages * p.hkv, BLK, HD, kChunk);
   if (st != BSA_OK) return st;
-  st = launch_dependent("paged attention launch", kern, unsigned(c.plan.units) * unsigned(c.plan.S), kThreads, smem, 1,
-                        c.stream, mq, mk, mv, p);
-  if (st != BSA_OK) return st;
+  st = launch_dependent("paged attention launch", kern, unsigned(c.plan.units) * unsigned(c.plan.S), kThreads, smem,
+                        ALONE ? unsigned(c.plan.S) : 1u, c.stream, mq, mk, mv, p);
+  if (st != BSA_OK || ALONE) return st;
   if constexpr (TREE) {
     const unsigned tb = unsigned(p.T + kJoinWarps - 1) / kJoinWarps;
     return launch_dependent("tree join launch", join_tree_kernel<BLK, HD>, unsigned(c.heads) * tb, kJoinWarps * 32, 0, 1,
@@ -1283,13 +1396,15 @@ int launch_rows(const Call& c, const Params& p) {
 
 template <int BLK, int HD, bool TREE>
 int launch(const Call& c, const Params& p) {
-  return p.rows <= kFew ? launch_rows<BLK, HD, TREE, true>(c, p) : launch_rows<BLK, HD, TREE, false>(c, p);
+  if constexpr (!TREE)
+    if (c.plan.alone) return launch_rows<BLK, HD, false, true, true>(c, p);
+  return p.rows <= kFew ? launch_rows<BLK, HD, TREE, true, false>(c, p) : launch_rows<BLK, HD, TREE, false, false>(c, p);
 }
 
 bool aligned(const void* x, uintptr_t a) { return (reinterpret_cast<uintptr_t>(x) % a) == 0; }
 
 // What both entry points check of the sizes; workspace sizes are 0 where it fails.
-int check_sizes(const bsa_layout* layout, int batch, int heads, int kv_heads, int T, int d) {
+int check_sizes(const bsa_layout* layout, int batch, int heads, int kv_heads, int T, int d, bool step) {
   if (!layout) return set_error(BSA_ERR_INVALID_ARG, "layout is NULL");
   if (layout->B != 64 && layout->B != 128) return set_error(BSA_ERR_UNSUPPORTED, "B must be 64 or 128");
   if (d != 64 && d != 128) return set_error(BSA_ERR_UNSUPPORTED, "d must be 64 or 128");
@@ -1301,7 +1416,7 @@ int check_sizes(const bsa_layout* layout, int batch, int heads, int kv_heads, in
   if (H % layout->L) return set_error(BSA_ERR_SHAPE, "query heads per sequence must be a multiple of layout_heads");
   if (T < 1 || T > kMaxT) return set_error(BSA_ERR_UNSUPPORTED, "the tree must have 1 to 128 tokens");
   if (int64_t(H / hkv) * T > INT32_MAX / 2) return set_error(BSA_ERR_SHAPE, "too many query rows");
-  const Plan p = plan_of(layout, batch, heads, kv_heads, T);
+  const Plan p = plan_of(layout, batch, heads, kv_heads, T, step);
   if (int64_t(p.units) * p.S > INT32_MAX || int64_t(heads) * ((T + kJoinWarps - 1) / kJoinWarps) > INT32_MAX / 2)
     return set_error(BSA_ERR_SHAPE, "too many query rows");
   return BSA_OK;
@@ -1309,9 +1424,9 @@ int check_sizes(const bsa_layout* layout, int batch, int heads, int kv_heads, in
 
 int check_call(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table, int max_blocks,
                int num_pages, const int32_t* lengths, const bsa_layout* layout, int batch, int heads, int kv_heads,
-               int T, int d, float scale, const void* o, const float* lse) {
+               int T, int d, float scale, const void* o, const float* lse, bool step) {
   if (!layout) return set_error(BSA_ERR_INVALID_ARG, "layout is NULL");
-  const int st = check_sizes(layout, batch, heads, kv_heads, T, d);
+  const int st = check_sizes(layout, batch, heads, kv_heads, T, d, step);
   if (st != BSA_OK) return st;
   if (max_blocks < layout->nb) return set_error(BSA_ERR_SHAPE, "max_blocks is smaller than the layout's blocks");
   if (num_pages < 1 || int64_t(num_pages) * (kv_heads / batch) > INT32_MAX)
@@ -1330,7 +1445,7 @@ int run(bool tree, const void* q, const void* k_tree, const void* v_tree, const 
         const int32_t* page_table, int max_blocks, int num_pages, const int32_t* lengths, const int32_t* parents,
         const bsa_layout* layout, int T, int batch, int heads, int kv_heads, int d, float scale, void* o, float* lse,
         float* weights, size_t weights_stride, void* workspace, size_t workspace_bytes, void* stream) {
-  const Plan pl = plan_of(layout, batch, heads, kv_heads, T);
+  const Plan pl = plan_of(layout, batch, heads, kv_heads, T, !tree);
   const Offsets of = offsets_of(pl, layout, heads, d, !tree);
   if (!workspace || !aligned(workspace, 16))
     return set_error(BSA_ERR_INVALID_ARG, "workspace must be non-null and 16-byte aligned");
@@ -1394,14 +1509,14 @@ extern "C" {
 
 size_t bsa_decode_weights_workspace_bytes(const bsa_layout* layout, int batch, int heads, int kv_heads, int d) {
   using namespace bsa::paged;
-  if (check_sizes(layout, batch, heads, kv_heads, 1, d) != BSA_OK) return 0;
-  return offsets_of(plan_of(layout, batch, heads, kv_heads, 1), layout, heads, d, true).total;
+  if (check_sizes(layout, batch, heads, kv_heads, 1, d, true) != BSA_OK) return 0;
+  return offsets_of(plan_of(layout, batch, heads, kv_heads, 1, true), layout, heads, d, true).total;
 }
 
 size_t bsa_decode_tree_workspace_bytes(const bsa_layout* layout, int batch, int heads, int kv_heads, int T, int d) {
   using namespace bsa::paged;
-  if (check_sizes(layout, batch, heads, kv_heads, T, d) != BSA_OK) return 0;
-  return offsets_of(plan_of(layout, batch, heads, kv_heads, T), layout, heads, d, false).total;
+  if (check_sizes(layout, batch, heads, kv_heads, T, d, false) != BSA_OK) return 0;
+  return offsets_of(plan_of(layout, batch, heads, kv_heads, T, false), layout, heads, d, false).total;
 }
 
 int bsa_decode_weights(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
@@ -1410,7 +1525,7 @@ int bsa_decode_weights(const void* q, const void* k_cache, const void* v_cache, 
                        size_t weights_stride, void* workspace, size_t workspace_bytes, void* stream) {
   using namespace bsa;
   const int st = paged::check_call(q, k_cache, v_cache, page_table, max_blocks, num_pages, positions, layout, batch,
-                                   heads, kv_heads, 1, d, scale, o, lse);
+                                   heads, kv_heads, 1, d, scale, o, lse, true);
   if (st != BSA_OK) return st;
   if (!weights || !paged::aligned(weights, 4))
     return set_error(BSA_ERR_INVALID_ARG, "weights must be non-null and 4-byte aligned");
@@ -1426,7 +1541,7 @@ int bsa_decode_tree(const void* q, const void* k_tree, const void* v_tree, const
                     float scale, void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
   using namespace bsa;
   const int st = paged::check_call(q, k_cache, v_cache, page_table, max_blocks, num_pages, lengths, layout, batch, heads,
-                                   kv_heads, T, d, scale, o, lse);
+                                   kv_heads, T, d, scale, o, lse, false);
   if (st != BSA_OK) return st;
   if (!k_tree || !v_tree || !parents) return set_error(BSA_ERR_INVALID_ARG, "null pointer");
   if (!paged::aligned(k_tree, 16) || !paged::aligned(v_tree, 16))

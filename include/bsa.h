@@ -313,8 +313,8 @@ size_t bsa_decode_weights_workspace_bytes(const bsa_layout* layout, int batch, i
  * Requirements as for bsa_decode, and: num_pages * Hkv below 2^31; workspace
  * 16-byte aligned and of at least the bytes above, used by no other call at
  * the same time; weights not overlapping any other argument.  The sums' order
- * is fixed, so a call gives the same bits every time.  Enqueues two kernels
- * and returns; no allocation. */
+ * is fixed, so a call gives the same bits every time.  Enqueues one kernel (a
+ * cluster launch, where rows are short) or two and returns; no allocation. */
 int bsa_decode_weights(const void* q, const void* k_cache, const void* v_cache,
                        const int32_t* page_table, int max_blocks, int num_pages,
                        const int32_t* positions, const bsa_layout* layout, int batch,
