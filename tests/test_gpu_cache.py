@@ -809,6 +809,87 @@ def test_calls_on_two_streams_at_once_and_in_a_graph():
     lay.close()
 
 
+def test_long_steps_and_cuts_refuse_replay_and_run_on_two_streams():
+    """Rows too long for one kernel: a bad page and a bad length refuse their own sequence alone, calls on two
+    streams and replayed ones give the bits of one call after the other."""
+    n, B, batch, H, G, d, budget = 4500, 64, 2, 4, 2, 64, 1500
+    lay = _layout(OL.BAND_GLOBAL, n, B, 1, dict(window=-(-n // B), global_first=0))
+    kc, vc, table, th = _paged(batch, G, n, B, d, 210)
+    q = to_device_bf16(inputs.normal_bf16_bits((batch * H, d), 211))
+    pos = torch.tensor([n - 1, 3000], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([n, 3001], dtype=torch.int32, device="cuda")
+    w0 = torch.rand((batch * G, n), device="cuda")
+
+    class Out:
+        pass
+
+    def bufs():
+        x = Out()
+        x.kc, x.vc, x.w = kc.clone(), vc.clone(), w0.clone()
+        x.o, x.lse = torch.zeros_like(q), torch.zeros(batch * H, device="cuda")
+        x.wo, x.to = torch.zeros((batch * G, n), device="cuda"), torch.zeros((batch * G, n), dtype=torch.int32, device="cuda")
+        x.lo = lens.clone()
+        x.ws = torch.empty(max(bsa.bsa_decode_weights_workspace_bytes(lay.handle, batch, batch * H, batch * G, d),
+                               bsa.bsa_evict_workspace_bytes(lay.handle, batch, batch * G, budget)),
+                           dtype=torch.uint8, device="cuda")
+        return x
+
+    def calls(x, tab=table, at=pos, ln=lens, stream=None):
+        # one workspace for all: the calls of a stream follow each other
+        for _ in range(2):
+            bsa.decode_weights(q, x.kc, x.vc, tab, at, lay, batch, x.w, o=x.o, lse=x.lse, workspace=x.ws, stream=stream)
+        bsa.evict(x.kc, x.vc, tab, ln, x.w, lay, budget, 100, weights_out=x.wo, tokens_out=x.to, lengths_out=x.lo,
+                  workspace=x.ws, stream=stream)
+
+    names = ("o", "lse", "w", "kc", "vc", "wo", "to", "lo")
+
+    def same(x, y):
+        return all(torch.equal(getattr(x, a).view(torch.uint8), getattr(y, a).view(torch.uint8)) for a in names)
+
+    ref, a, b, c = bufs(), bufs(), bufs(), bufs()
+    calls(ref)
+    torch.cuda.synchronize()
+    bsa.bsa_get_status(lay.handle)
+    for s, x in ((torch.cuda.Stream(), a), (torch.cuda.Stream(), b)):
+        calls(x, stream=s)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    assert same(a, ref) and same(b, ref)
+    with torch.cuda.graph(g):
+        calls(c)
+    pos.fill_(2600)
+    lens.fill_(2601)
+    fresh = bufs()
+    for name in names:
+        getattr(c, name).copy_(getattr(fresh, name))
+    torch.cuda.synchronize()
+    g.replay()
+    calls(fresh)
+    torch.cuda.synchronize()
+    bsa.bsa_get_status(lay.handle)
+    assert same(c, fresh)
+    # sequence 0 refused: by a page that does not exist, and by a position and length past the end
+    past = torch.tensor([n + 1, 2601], dtype=torch.int32, device="cuda")
+    bad = table.clone()
+    bad[0, 7] = kc.shape[0]
+    for tab, at, ln in ((bad, pos, lens), (table, past - 1, past)):
+        x = bufs()
+        calls(x, tab, at, ln)
+        torch.cuda.synchronize()
+        with pytest.raises(bsa.BsaError):
+            bsa.bsa_get_status(lay.handle)
+        assert torch.all(x.o[:H] == 0) and torch.all(torch.isneginf(x.lse[:H])) and torch.equal(x.w[:G], w0[:G])
+        assert torch.all(x.wo[:G] == 0) and torch.all(x.to[:G] == 0) and x.lo.tolist() == [-1, budget]
+        mine = table[0].long()
+        assert torch.equal(x.kc[mine].view(torch.int16), kc[mine].view(torch.int16))
+        for name in ("o", "lse"):
+            assert torch.equal(getattr(x, name)[H:], getattr(fresh, name)[H:])
+        for name in ("w", "wo", "to"):
+            assert torch.equal(getattr(x, name)[G:], getattr(fresh, name)[G:])
+    del g
+    lay.close()
+
+
 def test_wrong_tensors_are_refused():
     lay, q, kt, vt, kc, vc, table, lens, par = _small_tree(150)
     good = (q, kt, vt, kc, vc, table, lens, par)
