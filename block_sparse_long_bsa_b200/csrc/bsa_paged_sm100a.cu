@@ -23,7 +23,8 @@
 // leaves its unnormalised O, m and l in the caller's workspace; the step
 // leaves the scores too.
 // Kernel 2 joins the runs of each row.  The tree's rows add their ancestors
-// there (before its wait for kernel 1, as far as its blocks find room beside that), at most T keys each, on the plain cores in fp32: an ancestor's key
+// there (before its wait for kernel 1, as far as its blocks find room beside
+// that), at most T keys each, on the plain cores in fp32: an ancestor's key
 // and value are read by the rows that descend from it and by no others, so a
 // branch's infinity cannot reach another branch.  The step's kernel 2 also
 // turns the scores into weights, p = exp2(s scale log2 e - M) / L.  Short steps
@@ -36,11 +37,11 @@
 // step is bound by memory either way, but the large tiles, nearly all of them
 // empty, kept the tensor cores 60 % busy, and a server's GPU runs at its power
 // limit: 16 x 16K steps that follow each other for seconds took 181 to 193 us
-// each with the clocks at 1.45 to 1.6 GHz, and take 162 at 1.8; a few at a
-// time 164 and 160.  (128 rows of S^T are 64 keys and whatever lies behind them in shared
-// memory, which nobody reads.)  With 8 rows both ways take the same time,
-// 41.1 and 42.0 us over 2 x 131K, 82.8 and 83.1 over 8 x 16K; with 1 row 28.0
-// and 29.2, 80.9 and 81.5.
+// each with the clocks at 1.45 to 1.6 GHz, and take 158 to 162 at 1.8; a few at
+// a time 164 and 160.  (128 rows of S^T are 64 keys and whatever lies behind
+// them in shared memory, which nobody reads.)  With 8 rows this way and the
+// other take 41.1 and 42.0 us over 2 x 131K, 82.8 and 83.1 over 8 x 16K; with 1
+// row 28.0 and 29.2, 80.9 and 81.5.
 //
 // Roles of kernel 1 (192 threads, two CTAs per SM): warp 0 looks the pages up
 // and issues the TMA loads, warp 1 issues the products, warps 2-5 hold one
