@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // a later layout row has rows only if the tree is deep enough to reach it
     if (grp > 0) {
       const int len = p.lengths[b];
-      const int need = (len / BLK + grp) * BLK - len;
+      const int need = grp * BLK - len % BLK;     // depth at which the layout row begins
       skip = len < 0 || len > p.n || len / BLK + grp >= p.nb || need > p.T - 1;
       if (!skip)
         skip = need > deepest(p.parents + size_t(b) * p.T, p.T, reinterpret_cast<volatile int8_t*>(smem + S::kOffJump),
@@ -421,9 +421,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == 0) {
     Run r{};
     const int t = p.lengths[b];
-    const int ctx = TREE ? t : t + 1;             // cached keys that exist
     const int row = t / BLK + grp;
     if (!skip && (TREE ? t >= 0 && t <= p.n : t >= 0 && t < p.n) && row < p.nb) {
+      const int ctx = TREE ? t : t + 1;           // cached keys that exist
       const size_t at = size_t(f0 % p.L) * p.nb + row;
       r.start = p.row_ptr[at];
       const int full = p.row_ptr[at + 1] - r.start;
@@ -1108,14 +1108,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) join_step_kernel(const Par
   const int tile = x % p.tiles, hg = x / p.tiles;           // hg over batch * head groups
   const int g = p.H / p.hkv;
   const int b = hg / p.hg, h0 = (hg - b * p.hg) * p.hpt;    // the block's query head(s) in the sequence
-  const int t = p.lengths[b];
-  const bool in = t >= 0 && t < p.n;
+  // A refused position counts as -1, below every key: the keys that a thread
+  // does not have are INT32_MAX, which a position of that value would reach.
+  const int pos = p.lengths[b];
+  const bool in = pos >= 0 && pos < p.n;
+  const int t = in ? pos : -1;
   const size_t at0 = size_t((b * p.H + h0) % p.L) * p.nb + (in ? t / BLK : 0);
   const int start = p.row_ptr[at0], list = in ? (p.row_ptr[at0 + 1] - start) * BLK : 0;
   const int kv = h0 / g, first = p.L == 1 ? h0 : kv * g;    // first query head of the group
   float* const w = p.weights + size_t(b * p.hkv + kv) * p.weights_stride;
   // what needs no result of kernel 1 comes before the wait for it
-  int u[kGroups];                                           // first of four keys; past t if there are none
+  int u[kGroups];                                           // first of four keys; INT32_MAX if there are none
   float old[kGroups][4];
 #pragma unroll
   for (int i = 0; i < kGroups; ++i) {

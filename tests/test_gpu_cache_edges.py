@@ -1,0 +1,98 @@
+"""The cache operators' corners on the GPU.  Tolerances as derived in test_gpu_cache.py."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import block_sparse_long_bsa_b200 as bsa
+from block_sparse_long_bsa_b200 import inputs
+from oracle import layouts as OL
+
+from gpu_common import to_device_bf16
+from test_gpu_cache import DYADIC, _layout, _paged
+
+pytestmark = pytest.mark.gpu
+
+INT_MAX, INT_MIN = 2 ** 31 - 1, -2 ** 31
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    bsa.load_library()
+
+
+def _i32(*x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------ indices at the ends of 32 bits
+
+@pytest.mark.parametrize("kind,n,L,pat", [
+    (OL.DYADIC, 1024, 1, DYADIC),                                             # short rows: one kernel
+    (OL.BAND_GLOBAL, 4500, 1, dict(window=71, global_first=0)),               # long rows: two
+    (OL.RANDOM, 9000, 4, dict(density=0.6, seed=3)),                          # and a route for each head
+])
+def test_step_refuses_positions_at_the_ends_of_32_bits(kind, n, L, pat):
+    """The largest and the smallest position, as a server may mark a place of the batch that is not in use."""
+    B, batch, H, G, d = 64, 4, 4, 2, 64
+    lay = _layout(kind, n, B, L, pat)
+    kc, vc, table, _ = _paged(batch, G, n, B, d, 300)
+    q = to_device_bf16(inputs.normal_bf16_bits((batch * H, d), 301))
+    w0 = torch.rand((batch * G, n), device="cuda")
+    ref = w0.clone()
+    o_ref, lse_ref = bsa.decode_weights(q, kc, vc, table, _i32(5, n - 1, 700, 700), lay, batch, ref)
+    w = w0.clone()
+    o, lse = bsa.decode_weights(q, kc, vc, table, _i32(INT_MAX, n - 1, INT_MIN, INT_MAX - 1), lay, batch, w)
+    torch.cuda.synchronize()
+    with pytest.raises(bsa.BsaError):
+        bsa.bsa_get_status(lay.handle)
+    for b in range(batch):
+        rows, kv = slice(b * H, (b + 1) * H), slice(b * G, (b + 1) * G)
+        if b == 1:
+            assert torch.equal(o[rows], o_ref[rows]) and torch.equal(lse[rows], lse_ref[rows])
+            assert torch.equal(w[kv], ref[kv])
+        else:
+            assert torch.all(o[rows] == 0) and torch.all(torch.isneginf(lse[rows])) and torch.equal(w[kv], w0[kv])
+    lay.close()
+
+
+@pytest.mark.parametrize("n,budget", [(640, 100), (5000, 2000)])
+def test_tree_and_cut_refuse_lengths_at_the_ends_of_32_bits(n, budget):
+    B, batch, H, G, d, T = 64, 3, 2, 2, 64, 70
+    lay = _layout(OL.BAND_GLOBAL, n, B, 1, dict(window=n // B + 1, global_first=0))
+    kc, vc, table, _ = _paged(batch, G, n, B, d, 310)
+    q, kt, vt = (to_device_bf16(x) for x in inputs.qkv_bits(batch * H, batch * G, T, d, seeds=(311, 312, 313)))
+    par = torch.arange(-1, T - 1, dtype=torch.int32, device="cuda").repeat(batch, 1)
+    o_ref, lse_ref = bsa.decode_tree(q, kt, vt, kc, vc, table, _i32(1, 500, 1), par, lay)
+    lens = _i32(INT_MAX, 500, INT_MIN)
+    o, lse = bsa.decode_tree(q, kt, vt, kc, vc, table, lens, par, lay)
+    torch.cuda.synchronize()
+    with pytest.raises(bsa.BsaError):
+        bsa.bsa_get_status(lay.handle)
+    assert torch.equal(o[H:2 * H], o_ref[H:2 * H]) and torch.equal(lse[H:2 * H], lse_ref[H:2 * H])
+    for b in (0, 2):
+        rows = slice(b * H, (b + 1) * H)
+        assert torch.all(o[rows] == 0) and torch.all(torch.isneginf(lse[rows]))
+    # parents at the ends refuse their rows and what descends from them
+    far = par.clone()
+    far[1, 3], far[1, 60] = INT_MAX, INT_MIN
+    o, lse = bsa.decode_tree(q, kt, vt, kc, vc, table, _i32(1, 500, 1), far, lay)
+    torch.cuda.synchronize()
+    with pytest.raises(bsa.BsaError):
+        bsa.bsa_get_status(lay.handle)
+    assert torch.equal(o[H:2 * H, :3], o_ref[H:2 * H, :3]) and torch.all(torch.isneginf(lse[H:2 * H, 3:]))
+    assert torch.equal(o[2 * H:], o_ref[2 * H:])
+    w = torch.rand((batch * G, n), device="cuda")
+    keys = kc.clone()
+    wo, to = torch.full_like(w, 7.0), torch.full(w.shape, 7, dtype=torch.int32, device="cuda")
+    _, _, lo = bsa.evict(kc, vc, table, lens, w, lay, budget, 10, weights_out=wo, tokens_out=to)
+    torch.cuda.synchronize()
+    with pytest.raises(bsa.BsaError):
+        bsa.bsa_get_status(lay.handle)
+    assert lo.tolist() == [-1, min(500, budget), -1]
+    for b in (0, 2):
+        rows, mine = slice(b * G, (b + 1) * G), table[b].long()
+        assert torch.all(wo[rows] == 7) and torch.all(to[rows] == 7)
+        assert torch.equal(kc[mine].view(torch.int16), keys[mine].view(torch.int16))
+    lay.close()
