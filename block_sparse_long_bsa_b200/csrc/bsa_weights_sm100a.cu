@@ -53,9 +53,13 @@ constexpr int kThreads = 96 + 128 * kGroups;
 constexpr int kTileM = 128;          // keys of a tile
 constexpr int kQSlots = 2, kKSlots = 4;
 constexpr int kSBufs = 4;            // S buffers, one more than groups: the next product is ready in time
-// A group that is still at tile t lets the products get to t + 3, and the
-// producer is two items ahead of them: at most seven items are in use at once.
-constexpr int kItems = 8;
+// Items in use at once, where every item is one tile: a group gives the S
+// buffer of tile t back before it reads the last of its item's lse, and what
+// holds the products back then is the group's next tile, t + kGroups, whose
+// buffer they need at t + kGroups + kSBufs.  So they may have ended item
+// t + kGroups + kSBufs - 1, and the first warp writes kQSlots items further.
+constexpr int kItems = 16;
+static_assert(kItems >= kGroups + kSBufs + kQSlots, "an item's entry is written again only after its last reader");
 static_assert(kKSlots == kSBufs, "a finished product releases its K slot and fills its S buffer");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint64_t kWaitNs = 1000000000ull, kDrainNs = 200000000ull;

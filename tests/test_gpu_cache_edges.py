@@ -1,14 +1,16 @@
 """The cache operators' corners on the GPU.  Tolerances as derived in test_gpu_cache.py."""
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 
 import block_sparse_long_bsa_b200 as bsa
 from block_sparse_long_bsa_b200 import inputs
+from oracle import cache as OC
 from oracle import layouts as OL
 
 from gpu_common import to_device_bf16
-from test_gpu_cache import DYADIC, _layout, _paged
+from test_gpu_cache import DYADIC, _close_w, _e_p, _layout, _np, _paged
 
 pytestmark = pytest.mark.gpu
 
@@ -95,4 +97,32 @@ def test_tree_and_cut_refuse_lengths_at_the_ends_of_32_bits(n, budget):
         rows, mine = slice(b * G, (b + 1) * G), table[b].long()
         assert torch.all(wo[rows] == 7) and torch.all(to[rows] == 7)
         assert torch.equal(kc[mine].view(torch.int16), keys[mine].view(torch.int16))
+    lay.close()
+
+
+# ------------------------------------------------------------------ prompts whose work items are one tile
+
+@pytest.mark.parametrize("B,H,G,d,n,window", [
+    (128, 16, 16, 64, 16384, 0),        # one key block a row
+    (128, 16, 8, 128, 16384, 0),
+    (64, 16, 16, 64, 16000, 1),         # two, a tile
+    (64, 32, 16, 128, 16000, 1),        # and two query heads an item
+])
+def test_prompt_weights_of_rows_of_one_tile(B, H, G, d, n, window):
+    """14 and more items a block of threads, each one tile, and an lse of its own for every row, so that an item
+    read in another's place shows: every key against fp64, and the same bits every time."""
+    lay = _layout(OL.BAND_GLOBAL, n, B, 1, dict(window=window, global_first=0))
+    sets = OL.kept_sets(OL.BAND_GLOBAL, n, B, 1, window=window, global_first=0)
+    qb, kb, vb = inputs.qkv_bits(H, G, n, d, seeds=(320, 321, 322))
+    q, k, v = (to_device_bf16(x) for x in (qb, kb, vb))
+    _, lse = bsa.attention(q, k, v, lay)
+    lse += torch.from_numpy(np.random.default_rng(323).uniform(-3, 3, (H, n)).astype(np.float32)).cuda()
+    got = [bsa.attention_weights(q, k, lse, lay) for _ in range(6)]
+    torch.cuda.synchronize()
+    bsa.bsa_get_status(lay.handle)
+    assert all(torch.equal(x, got[0]) for x in got)
+    qh, kh, lse_h = _np(q), _np(k), _np(lse)
+    want = OC.prompt_weights(qh, kh, lse_h, sets, B, d ** -0.5)
+    # a thread's longest chain of additions: 2 x 32 of the diagonal, 2 x 8 of the rest, then under 16 joins
+    _close_w(_np(got[0]), want, _e_p(d ** -0.5, d, qh, kh, lse_h), lse_h, terms=96)
     lay.close()
