@@ -153,7 +153,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = Shape<BLK, HD, PACK>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_addr(smem);
+  // rounds of one item per CTA, every other one the other way round, so that
+  // no CTA has the longer row of each
+  auto item = [&](uint32_t round) -> uint32_t {
+    return round * gridDim.x + (round & 1u ? gridDim.x - 1u - blockIdx.x : blockIdx.x);
+  };
+  const uint32_t rounds = (p.items + gridDim.x - 1) / gridDim.x;
+  // an item's unit, query block and first query head, and its place in row_ptr:
+  // unit by unit, last row first (rows grow with their index, and a unit's keys stay in L2)
+  auto place = [&](uint32_t it, int& unit, int& i, int& f0) -> size_t {
+    unit = int(it / uint32_t(p.nb));
+    i = p.nb - 1 - int(it - uint32_t(unit) * uint32_t(p.nb));
+    f0 = (p.kv0 * p.upk + unit) * PACK;
+    return size_t(f0 % p.L) * p.nb + i;
+  };
+  // The sums of a CTA that gives up are not whole: all of them become -inf,
+  // which no sum of exponentials is, and the second kernel leaves their keys as they were.
+  auto spoil = [&]() {
+    for (uint32_t round = 0; round < rounds; ++round) {
+      const uint32_t it = item(round);
+      if (it >= p.items) continue;
+      int unit, i, f0;
+      const size_t at = place(it, unit, i, f0);
+      const int e0 = p.row_ptr[at], floats = (p.row_ptr[at + 1] - e0) * BLK;
+      float* const out = p.part + (int64_t(unit) * p.slots + (e0 - p.row_ptr[size_t(f0 % p.L) * p.nb])) * BLK;
+      for (int x = threadIdx.x; x < floats; x += kThreads) out[x] = -INFINITY;
+    }
+  };
   if (base & 1023u) {                // never expected: the swizzle needs 1024-byte aligned tiles
+    grid_wait();
+    spoil();
     if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
     return;
   }
@@ -207,14 +236,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     struct Row {
       int unit, i, f0, e0, len;          // e0, len: still in flight until the next step
     };
-    // unit by unit, last row first: rows grow with their index, and a unit's keys stay in L2
     auto find_row = [&](uint32_t it) -> Row {
       Row r{0, 0, 0, 0, -1};
       if (it < p.items) {
-        r.unit = int(it / uint32_t(p.nb));
-        r.i = p.nb - 1 - int(it - uint32_t(r.unit) * uint32_t(p.nb));
-        r.f0 = (p.kv0 * p.upk + r.unit) * PACK;
-        const size_t at = size_t(r.f0 % p.L) * p.nb + r.i;
+        const size_t at = place(it, r.unit, r.i, r.f0);
         r.e0 = p.row_ptr[at];
         r.len = p.row_ptr[at + 1];
       }
@@ -240,12 +265,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return w;
     };
-    // rounds of one item per CTA, every other one the other way round, so that
-    // no CTA has the longer row of each
-    auto item = [&](uint32_t round) -> uint32_t {
-      return round * gridDim.x + (round & 1u ? gridDim.x - 1u - blockIdx.x : blockIdx.x);
-    };
-    const uint32_t rounds = (p.items + gridDim.x - 1) / gridDim.x;
     Row cur = find_row(item(0)), next = find_row(item(1));
     Found mine = find_keys(cur);
     for (uint32_t round = 0; round < rounds && ok; ++round) {
@@ -460,6 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, S::kTmemCols);
   }
+  if (*abort_flag) spoil();
 }
 
 // w[kv][u] += the sums of u's block, unit by unit and row by row.  A block of
@@ -566,10 +586,11 @@ __global__ void __launch_bounds__(kAddThreads) add_rows_kernel(const Params p) {
   __syncthreads();
   s_sum[threadIdx.x] = t4;                       // [SL][4][BLK] floats
   __syncthreads();
-  // a wait that ran out left sums unwritten: nothing is added then
-  if (u >= p.n || (*reinterpret_cast<volatile uint32_t*>(p.status) & kStatusTimeout)) return;
+  if (u >= p.n) return;
   const float* const mine = f + sl * 4 * BLK + kl;
-  *out = old + (((mine[0] + mine[BLK]) + (mine[2 * BLK] + mine[3 * BLK])) + sum);
+  const float all = ((mine[0] + mine[BLK]) + (mine[2 * BLK] + mine[3 * BLK])) + sum;
+  if (all == -INFINITY) return;          // a wait ran out: see the first kernel
+  *out = old + all;
 }
 
 // Query heads of a unit: two for B = 64 when a group's heads pair off on one route.

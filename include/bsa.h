@@ -285,11 +285,14 @@ size_t bsa_attention_weights_workspace_bytes(const bsa_layout* layout, int heads
  * [heads][n][d] bf16; k [kv_heads][n][d] bf16; lse [heads][n] fp32; weights
  * fp32, rows weights_stride >= n floats apart, set to zero by the caller
  * before a prompt's first call.  All sums are fp32 in an order that the layout
- * fixes, so a call gives the same bits every time.  Requirements (checked
- * before launch; errors launch nothing): as for bsa_forward; workspace
- * 16-byte aligned and of at least the bytes above, used by no other call at
- * the same time.  Enqueues two kernels for every 64 MiB of kept blocks' sums
- * (none for a layout that keeps nothing) and returns; no allocation. */
+ * fixes, so a call gives the same bits every time.  A device wait that runs
+ * out (never expected) leaves the weights of the keys it concerns as they were
+ * and is reported by bsa_get_status; other calls are not affected.
+ * Requirements (checked before launch; errors launch nothing): as for
+ * bsa_forward; workspace 16-byte aligned and of at least the bytes above, used
+ * by no other call at the same time.  Enqueues two kernels for every 64 MiB of
+ * kept blocks' sums (none for a layout that keeps nothing) and returns; no
+ * allocation. */
 int bsa_attention_weights(const void* q, const void* k, const float* lse,
                           const bsa_layout* layout, int B, int n, int heads, int kv_heads,
                           int d, float scale, float* weights, size_t weights_stride,

@@ -126,3 +126,21 @@ def test_prompt_weights_of_rows_of_one_tile(B, H, G, d, n, window):
     # a thread's longest chain of additions: 2 x 32 of the diagonal, 2 x 8 of the rest, then under 16 joins
     _close_w(_np(got[0]), want, _e_p(d ** -0.5, d, qh, kh, lse_h), lse_h, terms=96)
     lay.close()
+
+
+def test_prompt_weights_do_not_depend_on_another_calls_time_out():
+    """A wait that ran out in another call on the layout stays in its status word until that is read: prompt
+    weights are added all the same."""
+    n, B, H, G, d = 700, 64, 4, 2, 64
+    lay = _layout(OL.DYADIC, n, B, 1, DYADIC)
+    q, k, v = (to_device_bf16(x) for x in inputs.qkv_bits(H, G, n, d, seeds=(330, 331, 332)))
+    _, lse = bsa.attention(q, k, v, lay)
+    want = bsa.attention_weights(q, k, lse, lay)
+    torch.cuda.synchronize()
+    bsa.bsa_get_status(lay.handle)
+    bsa.bsa_debug_timeout_probe(lay.handle, d, 2_000_000)
+    got = bsa.attention_weights(q, k, lse, lay)
+    with pytest.raises(bsa.BsaError) as e:
+        bsa.bsa_get_status(lay.handle)
+    assert e.value.status == 7 and float(want.min()) > 0 and torch.equal(got, want)
+    lay.close()
