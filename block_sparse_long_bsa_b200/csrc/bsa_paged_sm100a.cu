@@ -257,12 +257,19 @@ __host__ __device__ constexpr uint64_t flat_fixed(uint32_t k_bytes, uint32_t row
   return (uint64_t((k_bytes >> 4) & 0x3FFFu) << 16) | (uint64_t((row_bytes >> 4) & 0x3FFFu) << 32) | (uint64_t(1) << 46);
 }
 
-// What cutting a probability's low 16 bits off leaves, and (least > 0) never 0: an
-// infinite value that the row reads then has the same sign in both products
-// (a rounded first part could leave a negative rest, and 0 * inf is NaN).
-// P itself being 0, where exp2 underflows, is 0 * inf in the definition too.
-__device__ __forceinline__ float rest_of(uint32_t bits, float least) {
-  return fmaxf(__uint_as_float(bits) - __uint_as_float(bits & 0xffff0000u), least);
+// Two probabilities as two bf16 numbers each: their upper 16 bits and the
+// rounding of what those leave, at least 2^-20 of P: an infinite value that
+// the row reads then has the same sign in both products (a rounded first part
+// could leave a negative rest, and 0 * inf is NaN).  2^-20 P is far inside the
+// 2^-15 that the rounding may be off by, and a P of 0 gets nothing.  (Below
+// 2^-113 the rest may end as 0, below 2^-119 its rounding is that of the
+// smallest bf16 number, 2^-134.)
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+  float la, lb;
+  fma2(la, lb, a, b, 0x1p-20f, 0.f);
+  hi = __byte_perm(ua, ub, 0x7632);
+  lo = pack_bf16(fmaxf(a - __uint_as_float(ua & 0xffff0000u), la), fmaxf(b - __uint_as_float(ub & 0xffff0000u), lb));
 }
 
 // What a CTA of kernel 1 works on, found by one thread and shared.
@@ -702,9 +709,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         uint32_t hi[kFew / 2], lo[kFew / 2];
 #pragma unroll
         for (int x = 0; x < kFew; x += 2) {
-          const uint32_t a = __float_as_uint(pr[x]), bb = __float_as_uint(pr[x + 1]);
-          hi[x / 2] = __byte_perm(a, bb, 0x7632);
-          lo[x / 2] = pack_bf16(rest_of(a, x < vr ? 1e-30f : 0.f), rest_of(bb, x + 1 < vr ? 1e-30f : 0.f));
+          split2(pr[x], pr[x + 1], hi[x / 2], lo[x / 2]);
           l[x] += pr[x];
           l[x + 1] += pr[x + 1];
         }
@@ -768,9 +773,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     const bool mine = row < vr;
     const uint32_t lane_base = tmem + (uint32_t(q4 * 32) << 16);
     const float sl2 = p.scale_log2;
-    // A row that the tile only has room for gets P = 0, not the 1 of its zero
-    // scores, which would cost the tensor cores power.
-    const float least = mine ? 1e-30f : 0.f;
     float m2 = -INFINITY, l = 0.f;
     bool ok = true;
     for (int c = 0; c < nch; ++c) {
@@ -810,6 +812,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         alpha = ex2(m2 - mb);
         m2 = mb;
       }
+      // (a row that the tile only has room for gets P = 0, not the 1 of its zero
+      // scores, which would cost the tensor cores power)
       const float neg_m = !mine ? -INFINITY : m2 == -INFINITY ? 0.f : -m2;
       float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
@@ -844,9 +848,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         uint32_t hi[16], lo[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const uint32_t a = __float_as_uint(sv[x * 32 + 2 * e]), bb = __float_as_uint(sv[x * 32 + 2 * e + 1]);
-          hi[e] = __byte_perm(a, bb, 0x7632);
-          lo[e] = pack_bf16(rest_of(a, least), rest_of(bb, least));
+          split2(sv[x * 32 + 2 * e], sv[x * 32 + 2 * e + 1], hi[e], lo[e]);
         }
         tmem_st16(s_col + x * 16, hi);
         tmem_st16(s_col + 32 + x * 16, lo);

@@ -7,10 +7,11 @@ torch = pytest.importorskip("torch")
 import block_sparse_long_bsa_b200 as bsa
 from block_sparse_long_bsa_b200 import inputs
 from oracle import cache as OC
+from oracle import decode as OD
 from oracle import layouts as OL
 
-from gpu_common import to_device_bf16
-from test_gpu_cache import DYADIC, _close_w, _e_p, _layout, _np, _paged
+from gpu_common import bf16_half_ulp, to_device_bf16
+from test_gpu_cache import DYADIC, _close_lse, _close_w, _e_p, _layout, _np, _paged
 
 pytestmark = pytest.mark.gpu
 
@@ -143,4 +144,83 @@ def test_prompt_weights_do_not_depend_on_another_calls_time_out():
     with pytest.raises(bsa.BsaError) as e:
         bsa.bsa_get_status(lay.handle)
     assert e.value.status == 7 and float(want.min()) > 0 and torch.equal(got, want)
+    lay.close()
+
+
+# ------------------------------------------------------------------ values that meet a probability of zero
+
+# op, tokens of the layout, B, query heads a key/value head (or drafted tokens), d
+ZERO = [("step", 1000, 64, 2, 64), ("step", 5000, 64, 2, 128), ("step", 5000, 128, 8, 64), ("step", 3000, 64, 16, 128),
+        ("tree", 1000, 64, 3, 64), ("tree", 3000, 128, 5, 128), ("tree", 1000, 64, 40, 128), ("tree", 3000, 128, 70, 64)]
+
+
+def _zero_case(case, seed):
+    op, n, B, m, d = case
+    G, H, T = 2, (2 * m if op == "step" else 2), (1 if op == "step" else m)
+    lay = _layout(OL.BAND_GLOBAL, n, B, 1, dict(window=n // B + 1, global_first=0))
+    sets = OL.kept_sets(OL.BAND_GLOBAL, n, B, 1, window=n // B + 1, global_first=0)
+    kc, vc, table, th = _paged(1, G, n, B, d, seed)
+    q, kt, vt = (to_device_bf16(x) for x in inputs.qkv_bits(H, G, T, d, seeds=(seed + 1, seed + 2, seed + 3)))
+    end = n - T
+    par = np.arange(-1, T - 1, dtype=np.int32)[None]
+
+    def run():
+        if op == "step":
+            w = torch.zeros((G, n), device="cuda")
+            out = bsa.decode_weights(q[:, 0].contiguous(), kc, vc, table, _i32(end - 1), lay, 1, w)
+        else:
+            out = bsa.decode_tree(q, kt, vt, kc, vc, table, _i32(end), torch.from_numpy(par).cuda(), lay)
+        torch.cuda.synchronize()
+        bsa.bsa_get_status(lay.handle)
+        return [_np(x) for x in out]
+
+    def oracle(values, drafted):
+        kh = np.nan_to_num(_np(kc), neginf=-np.inf)
+        if op == "step":
+            return OD.decode_step(_np(q)[:, 0], kh, values, th, [end - 1], sets, B, d ** -0.5)
+        return OC.tree(_np(q), _np(kt), drafted, kh, values, th, [end], par, sets, B, d ** -0.5)
+
+    return lay, q, kt, vt, kc, vc, table, end, run, oracle
+
+
+@pytest.mark.parametrize("case", ZERO)
+def test_large_values_of_keys_without_weight_add_nothing(case):
+    """Keys at minus infinity whose values are as large as bf16 holds: all of the first three chunks, a few later
+    ones, and a whole chunk in between."""
+    op, n, B, m, d = case
+    lay, q, kt, vt, kc, vc, table, end, run, oracle = _zero_case(case, 340)
+    q[:, :, 1] = q[:, :, 1].abs() + 0.5
+    token = torch.arange(-(-n // B) * B, device="cuda")
+    out = (token < 192) | (token % 97 == 5) | ((token >= 640) & (token < 704))
+    out = out.view(-1, B)[:, None, :]
+    pages = table[0].long()
+    kc[pages, :, :, 1] = torch.where(out, float("-inf"), kc[pages, :, :, 1])
+    vc[pages] = torch.where((out & (token.view(-1, B)[:, None] < end))[..., None], 2.0 ** 127, vc[pages])
+    vc[pages, :, :, 0] *= torch.where(out, -1.0, 1.0).to(torch.bfloat16)
+    o, lse = run()
+    vh, vth = np.nan_to_num(_np(vc)), _np(vt)
+    o_ref, lse_ref = oracle(vh, vth)
+    o_abs, _ = oracle(np.abs(vh), np.abs(vth))
+    assert np.abs(o_ref).max() < 10
+    kh = np.nan_to_num(_np(kc), neginf=0).reshape(-1, d)
+    e_p = _e_p(d ** -0.5, d, _np(q), np.concatenate([kh, _np(kt).reshape(-1, d)]), lse_ref)
+    _close_lse(lse, lse_ref, e_p)
+    bound = bf16_half_ulp(o) + 2 * (e_p + 2.0 ** -15) * o_abs
+    assert np.all(np.abs(o - o_ref) <= bound), (np.abs(o - o_ref) / bound).max()
+    lay.close()
+
+
+@pytest.mark.parametrize("case", ZERO)
+def test_infinite_values_of_equal_keys(case):
+    """All probabilities exactly a power of two, so that their second parts are the smallest there are: an infinite
+    value still gives an infinity of its sign, and nothing to the other columns."""
+    lay, q, kt, vt, kc, vc, table, end, run, oracle = _zero_case(case, 350)
+    q.zero_()
+    o, _ = run()
+    vc[table[0, 1].long(), :, 7, 3], vc[table[0, 2].long(), :, 9, 4] = float("inf"), float("-inf")
+    o2, lse2 = run()
+    assert np.isfinite(o).all() and np.isfinite(lse2).all()
+    assert np.all(o2[..., 3] == np.inf) and np.all(o2[..., 4] == -np.inf)
+    o2[..., 3:5] = o[..., 3:5]
+    assert np.array_equal(o, o2)
     lay.close()
