@@ -171,8 +171,12 @@ def _stream(s) -> int:
         try:
             import torch
             if torch.cuda.is_initialized():
-                _raw_stream = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-                return _raw_stream[0](_raw_stream[1]())
+                # torch's internal names; one that lacks them is asked for the Stream below
+                current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                device = getattr(torch._C, "_cuda_getDevice", None)
+                if current and device:
+                    _raw_stream = current, device
+                    return current(device())
             if torch.cuda.is_available():
                 return torch.cuda.current_stream().cuda_stream
         except ImportError:
