@@ -501,6 +501,8 @@ def _workspace(layout: "Layout", workspace, stream, bytes_of, *sizes):
     """The given workspace, or a new one of ``bytes_of(handle, *sizes)`` bytes
     that torch holds for ``stream``; (tensor, bytes)."""
     if workspace is None:
+        if layout.device < 0:
+            raise BsaError(1, "layout was built host-only (device = -1)")
         import torch
         with _on(stream):
             workspace = torch.empty(max(bytes_of(layout.handle, *sizes), 16), dtype=torch.uint8,

@@ -142,3 +142,22 @@ def test_sizes_that_pass_32_bits_are_refused_not_wrapped(lay):
     assert bsa.bsa_evict_workspace_bytes(lay.handle, 1, (1 << 31) - 1, 10) == 0
     assert bsa.bsa_attention_weights_workspace_bytes(lay.handle, (1 << 30), 1 << 30) == 0
     assert ctypes.sizeof(ctypes.c_size_t) == 8
+
+
+def test_the_conveniences_refuse_a_host_only_layout_as_the_calls_do():
+    torch = pytest.importorskip("torch")
+    only = bsa.Layout(OL.BAND_GLOBAL, 200, 64, 1, -1, window=4, global_first=0)
+    q, k, lse = torch.zeros((2, 200, 64)).bfloat16(), torch.zeros((1, 200, 64)).bfloat16(), torch.zeros((2, 200))
+    cache, table, one = torch.zeros((4, 1, 64, 64)).bfloat16(), torch.zeros((1, 4)).int(), torch.zeros(1).int()
+    w, row, tree = torch.zeros((1, 200)), q[:, 0].contiguous(), q[:, :3].contiguous()
+    own = torch.zeros(1 << 16, dtype=torch.uint8)
+    for more in ({}, {"workspace": own}):
+        for call in (lambda: bsa.attention_weights(q, k, lse, only, **more),
+                     lambda: bsa.decode_weights(row, cache, cache, table, one, only, 1, w, **more),
+                     lambda: bsa.evict(cache, cache, table, one, w, only, 100, **more),
+                     lambda: bsa.decode_tree(tree, k[:, :3].contiguous(), k[:, :3].contiguous(), cache, cache, table, one,
+                                             torch.zeros((1, 3)).int() - 1, only, **more)):
+            with pytest.raises(bsa.BsaError, match="host-only") as e:
+                call()
+            assert e.value.status == INVALID
+    only.close()
