@@ -48,6 +48,7 @@ constexpr int kBatch = 8;                       // loads of a thread in flight
 constexpr int kMaxCluster = 8, kSlotsPerBlock = kBatch * kSelThreads;
 constexpr int kKeysInSmem = 48 * 1024;          // a block with more slots recomputes its keys in every pass
 constexpr int kMoveThreads = 256;
+constexpr int kMaxSlots = 1 << 30;              // of a layout: a thread's next slots stay inside 32 bits
 
 struct Params {
   __nv_bfloat16* kc;
@@ -422,6 +423,7 @@ int check_sizes(const bsa_layout* layout, int batch, int kv_heads, int budget) {
   if (batch < 1 || kv_heads < 1) return set_error(BSA_ERR_SHAPE, "batch and kv_heads must be >= 1");
   if (kv_heads % batch) return set_error(BSA_ERR_SHAPE, "kv_heads must be a multiple of batch");
   if (budget < 1) return set_error(BSA_ERR_SHAPE, "budget must be >= 1");
+  if (layout->n > kMaxSlots) return set_error(BSA_ERR_SHAPE, "n must be at most 2^30");
   if (int64_t(kv_heads) * std::max<int64_t>(kMaxCluster, (int64_t(layout->n) + kMoveThreads - 1) / kMoveThreads) >
       INT32_MAX)
     return set_error(BSA_ERR_SHAPE, "too many slots");

@@ -355,8 +355,8 @@ size_t bsa_evict_workspace_bytes(const bsa_layout* layout, int batch, int kv_hea
  * weights, weights_out fp32, rows of all four `stride` elements apart.  The
  * layout supplies the device, B, n and the status word (its kept blocks are
  * not read).  Requirements (checked before launch; errors launch nothing):
- * layout on the current device; B in {64, 128}; d in {64, 128}; batch,
- * kv_heads, budget, num_pages >= 1; kv_heads a multiple of batch;
+ * layout on the current device, n at most 2^30; B in {64, 128}; d in {64, 128};
+ * batch, kv_heads, budget, num_pages >= 1; kv_heads a multiple of batch;
  * 0 <= recent <= budget; max_blocks >= the layout's blocks; stride >= n;
  * pointers (but tokens) non-null, caches and workspace 16-byte aligned, the
  * rest 4-byte aligned; the outputs must not overlap the inputs, and no page

@@ -161,3 +161,12 @@ def test_the_conveniences_refuse_a_host_only_layout_as_the_calls_do():
                 call()
             assert e.value.status == INVALID
     only.close()
+
+
+def test_the_cut_refuses_layouts_past_2_to_the_30():
+    """Its threads step through the slots with 32-bit numbers; the caches of so many tokens would pass the GPU's memory."""
+    n = (1 << 30) + 1
+    long = bsa.Layout(OL.BAND_GLOBAL, n, 128, 1, -1, window=0, global_first=0)
+    assert bsa.bsa_evict_workspace_bytes(long.handle, 1, 1, 10) == 0
+    assert _status(bsa.bsa_evict, _evict_args(long, max_blocks=1 << 24, stride=n, batch=1, kv_heads=1)) == SHAPE
+    long.close()
