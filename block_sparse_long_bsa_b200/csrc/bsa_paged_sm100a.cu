@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       // whole cache that a tree straddles two blocks of is read once, not twice).
       if (!skip) {
         const size_t at = size_t(f0 % p.L) * p.nb + len / BLK;
-        const int blocks = (len + BLK - 1) / BLK;
+        const int blocks = len / BLK + (len % BLK != 0);
         skip = keeps_all(p, at, blocks) && keeps_all(p, at + grp, blocks);
       }
     }
@@ -1241,8 +1241,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) join_tree_kernel(const Par
     }
   }
   __syncwarp();
+  if (!bad && live && count > p.n - len) bad = true;   // past the layout's last position
   const int pos = bad ? 0 : len + count - 1;
-  if (pos >= p.n) bad = true;
   // the layout row of the token, and which of the blocks that its path lies in it keeps
   const int blk = pos / BLK, blk0 = bad ? 0 : len / BLK;
   const size_t at = size_t(f % p.L) * p.nb + blk;
@@ -1256,7 +1256,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) join_tree_kernel(const Par
   keeps = __reduce_or_sync(0xffffffffu, keeps);
   int grp = blk - blk0;                           // whose runs the row reads: see kernel 1
   if (live && !bad && grp > 0) {
-    const int blocks = (len + BLK - 1) / BLK;
+    const int blocks = len / BLK + (len % BLK != 0);
     if (keeps_all(p, at, blocks) && keeps_all(p, at - grp, blocks)) grp = 0;
   }
   // scores of the ancestors: 8 lanes a key, four keys at a time

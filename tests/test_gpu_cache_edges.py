@@ -11,7 +11,7 @@ from oracle import decode as OD
 from oracle import layouts as OL
 
 from gpu_common import bf16_half_ulp, to_device_bf16
-from test_gpu_cache import DYADIC, _close_lse, _close_w, _e_p, _layout, _np, _paged
+from test_gpu_cache import DYADIC, _close_lse, _close_o, _close_w, _e_p, _layout, _np, _paged
 
 pytestmark = pytest.mark.gpu
 
@@ -223,4 +223,47 @@ def test_infinite_values_of_equal_keys(case):
     assert np.all(o2[..., 3] == np.inf) and np.all(o2[..., 4] == -np.inf)
     o2[..., 3:5] = o[..., 3:5]
     assert np.array_equal(o, o2)
+    lay.close()
+
+
+# ------------------------------------------------------------------ a layout as long as 32 bits count
+
+def test_step_and_tree_at_the_end_of_the_longest_layout():
+    """2^31 - 1 tokens, each block for itself: a step at the last position, and a chain whose first token takes it;
+    the others lie past the end and are refused."""
+    n, B, H, G, d, T = INT_MAX, 128, 2, 1, 64, 5
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 20 GB of device memory")
+    lay = _layout(OL.BAND_GLOBAL, n, B, 1, dict(window=0, global_first=0))
+    kc, vc, _, _ = _paged(1, G, B, B, d, 360)
+    q, kt, vt = (to_device_bf16(x) for x in inputs.qkv_bits(2 * H, 2 * G, T, d, seeds=(361, 362, 363)))
+    table = torch.zeros((2, -(-n // B)), dtype=torch.int32, device="cuda")
+    par = torch.arange(-1, T - 1, dtype=torch.int32, device="cuda").repeat(2, 1)
+    o, lse = bsa.decode_tree(q, kt, vt, kc, vc, table, _i32(n - 1, n), par, lay)
+    torch.cuda.synchronize()
+    with pytest.raises(bsa.BsaError):
+        bsa.bsa_get_status(lay.handle)
+    assert torch.all(o[:H, 1:] == 0) and torch.all(torch.isneginf(lse[:H, 1:]))
+    assert torch.all(o[H:] == 0) and torch.all(torch.isneginf(lse[H:]))
+    end = (n - 1) % B                                # cached tokens of the last block
+    page = np.zeros((1, 1), np.int64)
+    sets, kh, vh = [[{0}]], _np(kc), _np(vc)
+    o_ref, lse_ref = OC.tree(_np(q)[:H, :1], _np(kt)[:G, :1], _np(vt)[:G, :1], kh, vh, page, [end],
+                             np.full((1, 1), -1), sets, B, d ** -0.5)
+    e_p = _e_p(d ** -0.5, d, _np(q), np.concatenate([kh.reshape(-1, d), _np(kt).reshape(-1, d)]), lse_ref)
+    _close_lse(_np(lse)[:H, :1], lse_ref, e_p)
+    _close_o(_np(o)[:H, :1], o_ref, e_p, np.concatenate([vh.reshape(-1, d), _np(vt).reshape(-1, d)]))
+    w = torch.zeros((G, n), device="cuda")
+    row = q[:H, 0].contiguous()
+    o, lse = bsa.decode_weights(row, kc, vc, table[:1], _i32(n - 1), lay, 1, w)
+    torch.cuda.synchronize()
+    bsa.bsa_get_status(lay.handle)
+    o_ref, lse_ref = OD.decode_step(_np(row), kh, vh, page, [end], sets, B, d ** -0.5)
+    e_p = _e_p(d ** -0.5, d, _np(row), kh, lse_ref)
+    _close_lse(_np(lse), lse_ref, e_p)
+    _close_o(_np(o), o_ref, e_p, vh)
+    want = OC.step_weights(_np(row), kh, page, [end], lse_ref, sets, B, d ** -0.5, end + 1)
+    bound = want * (2 * e_p + 2.0 ** -21 + H * 2.0 ** -24)
+    assert np.all(np.abs(_np(w[:, n - end - 1:]) - want) <= bound)
+    assert not torch.any(w[:, :n - end - 1])
     lay.close()
