@@ -1119,7 +1119,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) join_step_kernel(const Par
   const int start = p.row_ptr[at0], list = in ? (p.row_ptr[at0 + 1] - start) * BLK : 0;
   const int kv = h0 / g, first = p.L == 1 ? h0 : kv * g;    // first query head of the group
   float* const w = p.weights + size_t(b * p.hkv + kv) * p.weights_stride;
-  // what needs no result of kernel 1 comes before the wait for it
+  // What needs no result of kernel 1 comes before the wait for it: kernel 1
+  // lets this one start only once its own wait is over, so whatever the stream
+  // held before it has ended.  The running weights are read at L2, past any
+  // piece of them that this SM kept from the step before.
   int u[kGroups];                                           // first of four keys; INT32_MAX if there are none
   float old[kGroups][4];
 #pragma unroll
@@ -1130,7 +1133,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) join_step_kernel(const Par
 #pragma unroll
   for (int i = 0; i < kGroups; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) old[i][e] = u[i] <= t && u[i] + e <= t ? w[u[i] + e] : 0.f;
+    for (int e = 0; e < 4; ++e) old[i][e] = u[i] <= t && u[i] + e <= t ? __ldcg(w + u[i] + e) : 0.f;
   grid_wait();
   if (tile * kTileKeys >= list) return;
   float sum[kGroups][4] = {};

@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kAddThreads) add_rows_kernel(const Params p) {
   float* const f = reinterpret_cast<float*>(s_sum);
   grid_release();
   float* const out = p.weights + size_t(p.kv0 + kvl) * p.weights_stride + u;
-  const float old = u < p.n ? *out : 0.f;
+  const float old = u < p.n ? __ldcg(out) : 0.f;     // (the kernel ahead has waited for what wrote them)
   float4 t4 = make_float4(0.f, 0.f, 0.f, 0.f);   // this thread's slice of column sl
   float sum = 0.f;                               // of key kl of a long column sl
 #pragma unroll 1

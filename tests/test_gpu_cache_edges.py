@@ -267,3 +267,75 @@ def test_step_and_tree_at_the_end_of_the_longest_layout():
     assert np.all(np.abs(_np(w[:, n - end - 1:]) - want) <= bound)
     assert not torch.any(w[:, :n - end - 1])
     lay.close()
+
+
+# ------------------------------------------------------------------ running weights read early
+
+@pytest.mark.parametrize("kind,n,B,L,H,G,d,pat", [
+    (OL.BAND_GLOBAL, 20000, 64, 1, 4, 2, 64, dict(window=313, global_first=0)),    # two kernels, short rows of queries
+    (OL.BAND_GLOBAL, 9000, 128, 1, 32, 2, 64, dict(window=71, global_first=0)),    # 16 query heads a key/value head
+    (OL.RANDOM, 9000, 64, 4, 4, 2, 128, dict(density=0.6, seed=3)),                # a route for each head
+    (OL.DYADIC, 3000, 64, 1, 4, 2, 128, DYADIC),                                   # one kernel
+])
+def test_calls_that_follow_each_other_unsynchronised(kind, n, B, L, H, G, d, pat):
+    """Steps, trees, prompt weights and torch's own kernels that change the same running weights one after the other, with
+    nothing waited for in between: the bits of the same calls with the GPU waited for after each.  Rows of weights
+    lie an odd number of floats apart, so that blocks of threads share pieces of memory."""
+    batch, prompt = 2, 700
+    lay = _layout(kind, n, B, L, pat)
+    short = _layout(OL.DYADIC, prompt, B, 1, DYADIC)
+    kc, vc, table, _ = _paged(batch, G, n, B, d, 370)
+    qp, kp, vp = (to_device_bf16(x) for x in inputs.qkv_bits(batch * H, batch * G, prompt, d, seeds=(371, 372, 373)))
+    _, lse_p = bsa.attention(qp, kp, vp, short)
+    qs = [to_device_bf16(inputs.normal_bf16_bits((batch * H, d), 380 + i)) for i in range(12)]
+    at = [_i32(n - 1 - i, n // 2 + i) for i in range(12)]
+    w0 = torch.rand((batch * G, n + 5), device="cuda")
+    h = lay.handle
+    T = 7
+    trees = [[to_device_bf16(x) for x in inputs.qkv_bits(batch * H, batch * G, T, d, seeds=(390 + i, 410 + i, 430 + i))]
+             for i in range(12)]
+    parents = [_i32(*([-1] + [max(-1, j - 1 - (i + j) % 3) for j in range(1, T)]) * batch).view(batch, T) for i in range(12)]
+    ws = torch.empty(max(bsa.bsa_decode_weights_workspace_bytes(h, batch, batch * H, batch * G, d),
+                         bsa.bsa_decode_tree_workspace_bytes(h, batch, batch * H, batch * G, T, d),
+                         bsa.bsa_attention_weights_workspace_bytes(short.handle, batch * H, batch * G)),
+                     dtype=torch.uint8, device="cuda")
+
+    def run(wait):
+        w, q, pos, out = w0.clone(), torch.empty_like(qs[0]), torch.empty_like(at[0]), []
+        tree = [torch.empty_like(x) for x in trees[0] + [parents[0]]]
+        wait()
+        for i, (x, t) in enumerate(zip(qs, at)):
+            q.copy_(x)
+            pos.copy_(t)
+            wait()
+            for _ in range(2):
+                out += bsa.decode_weights(q, kc, vc, table, pos, lay, batch, w, workspace=ws)
+                wait()
+            for a, b in zip(tree, trees[i] + [parents[i]]):
+                a.copy_(b)
+            wait()
+            out += bsa.decode_tree(*tree[:3], kc, vc, table, pos - T, tree[3], lay, workspace=ws)
+            wait()
+            if i % 3 == 1:
+                w.mul_(0.75)
+                wait()
+            if i % 4 == 2:
+                bsa.attention_weights(qp, kp, lse_p, short, w, workspace=ws)
+                wait()
+                bsa.attention_weights(qp, kp, lse_p, short, w, workspace=ws)
+                wait()
+        torch.cuda.synchronize()
+        return [w] + out
+
+    want = run(torch.cuda.synchronize)
+    for _ in range(5):
+        got = run(lambda: None)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    tail = w0[:, n:]
+    for _ in range(4):
+        tail = tail * 0.75
+    assert torch.equal(want[0][:, n:], tail)
+    bsa.bsa_get_status(lay.handle)
+    bsa.bsa_get_status(short.handle)
+    lay.close()
+    short.close()
