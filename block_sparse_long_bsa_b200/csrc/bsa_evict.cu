@@ -149,7 +149,7 @@ __device__ __forceinline__ void move_slot(const Params& p, int row, int s, int4 
 // memory after a barrier.  Nothing read so is written again.  The loops are not
 // unrolled: a block runs through them once or a few times, and fetching their
 // instructions is what it would wait for.
-// HD > 0: the blocks go on to move the rows, and no second kernel runs.
+// HD > 0: C is 1, the block goes on to move the rows, and no second kernel runs.
 template <int HD>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int C) {
   extern __shared__ uint32_t s_keys[];
@@ -183,9 +183,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
   // the end of a row that is not refused
   auto finish = [&](int4 m) {
     if constexpr (HD > 0) {
-      if (tid == 0 && rank == 0 && row % p.hkv == 0) p.lengths_out[b] = m.x;
+      if (tid == 0 && row % p.hkv == 0) p.lengths_out[b] = m.x;
 #pragma unroll 1
-      for (int s0 = rank * kSelThreads; s0 < p.n; s0 += C * kSelThreads) move_slot<HD>(p, row, s0 + tid, m);
+      for (int s0 = 0; s0 < p.n; s0 += kSelThreads) move_slot<HD>(p, row, s0 + tid, m);
     } else if (tid == 0 && rank == 0) {
       p.meta[row] = m;
     }
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p, int
     hole0 += __popc(hb);
   }
   cluster_wait();                        // no block ends while another may still read its shared memory
-  if (HD > 0) cluster_sync();            // all blocks' lists are written
+  if (HD > 0) __syncthreads();           // the lists are written
   finish(make_int4(p.budget, newest, 0, 0));
 }
 
@@ -453,16 +453,20 @@ int launch(const Params& p, int rows, int d, cudaStream_t stream) {
     }
   }
   // blocks per row: one for each kSlotsPerBlock slots, so that a thread has one
-  // batch of them, while the GPU holds them two to an SM
+  // batch of them, while the GPU holds them two to an SM (a figure for speed
+  // alone: any number of blocks is right on any GPU)
   int C = 1;
   while (C < kMaxCluster && p.n > C * kSlotsPerBlock && rows * C <= 148) C *= 2;
   const int per = (p.n + C * 32 - 1) / (C * 32) * 32;
-  // One kernel where a row has one block and few slots or moves, at most
-  // min(budget, n - budget): a launch less on the host.  (us, two kernels and
-  // one: 8 rows of 1000 slots cut to 500 13.7 and 11.7, 256 of them 22.1 and
-  // 20.8; 256 rows of 4000 cut to 3900 20.5 and 16.9; but to 3700 22.4 and 24.1,
-  // 8 of 2000 cut to 1000 13.5 and 15.9, 16 of 32768 cut to 8192 42.5 and 46.6:
-  // a row's own block takes its slots 512 at a time.)
+  // One kernel where a row has one block and few slots or moves, of which there
+  // are at most min(budget, n - budget), n being what the host knows: a launch
+  // less, but a row's own block takes its slots 512 at a time.  (us on the GPU
+  // alone, in graphs, one kernel and two.  Slots, cut to a half: 256 rows of
+  // 1024 15.1 and 19.2, of 1100 21.1 and 21.4, of 1300 24.2 and 23.0; 8 rows of
+  // 1024 9.7 and 9.7, of 1100 13.4 and 11.0.  Moves, all slots full: 256 rows
+  // cut to 4096 by 100 24.9 and 27.8, by 128 26.1 and 28.6, by 256 32.3 and
+  // 33.8; 8 rows of 2000 cut by 64 10.6 and 9.9, by 128 11.1 and 10.4, by 256
+  // 12.9 and 10.4, launched one by one 11.9 and 13.4 by 128, 13.6 and 13.6 by 256.)
   const bool alone = C == 1 && (p.n <= 2 * kSelThreads || std::min(p.budget, p.n - p.budget) <= kSelThreads / 4);
   const auto select = !alone ? select_kernel<0> : d == 128 ? select_kernel<128> : select_kernel<64>;
   int st = launch_dependent("eviction select launch", select, unsigned(rows) * unsigned(C), kSelThreads,
