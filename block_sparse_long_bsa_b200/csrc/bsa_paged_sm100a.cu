@@ -18,8 +18,9 @@
 //   O += P V                   (tcgen05.mma, A = P from TMEM)
 // with P written as two bf16 numbers (its upper 16 bits and the rounding of what
 // they leave, within 2^-15 of P together) over the 64 columns of S, and two
-// products: the step is bound by the cache's bytes, so the second product
-// costs nothing that shows, and o is then rounded once, at its end.  A run
+// products: a step is bound by the cache's bytes, so the second product costs
+// nothing that shows there (10 % of a call where full tiles of tree rows run at
+// the power limit), and o is then rounded once, at its end.  A run
 // leaves its unnormalised O, m and l in the caller's workspace; the step
 // leaves the scores too.
 // Kernel 2 joins the runs of each row.  The tree's rows add their ancestors
@@ -77,10 +78,12 @@ constexpr float kLn2 = 0.693147180559945309f;
 constexpr uint64_t kWaitNs = 1000000000ull, kDrainNs = 200000000ull;
 
 // Runs of a unit: as many CTAs as the GPU holds at once (two on each of 148
-// SMs) shared out over the units, rounded down (8 runs a unit, 512 CTAs, took
-// 114 us for 64-token trees over 8 x 16K where 4, 256 CTAs, took 106), and no run
-// longer than kRunChunks, so that sequences of other lengths level out (16 x 16K
-// step: 2 runs of 128 chunks 176 us, 4 of 64 169, 8 of 32 176).
+// SMs: a figure for speed alone, fixed so that a host-only layout gives the same
+// workspace) shared out over the units, rounded down (twice as many: 64-token
+// trees over 8 x 16K 136 us for 130, 2 x 131K steps with a route a head 33.6 for
+// 28.4, chains 47.2 for 38.4), and no run longer than kRunChunks, so that
+// sequences of other lengths level out (16 x 16K step: 2 runs of 128 chunks 171
+// us, 4 of 64 162.6, 8 of 32 164.4; 32 x 8K 169, 158, 160; the trees 130, 130 and 137).
 constexpr int kSlots = 2 * 148;
 // A step of at most 8 query rows a unit and few chunks is one kernel, a
 // cluster of up to 8 CTAs per unit that joins its runs through shared memory:
@@ -162,7 +165,7 @@ struct Params {
   float* scores;               // step: [heads][max_row * B]
   uint32_t* status;
   size_t score_stride;
-  int n, nb, L, H, hkv, max_blocks, num_pages, max_row;
+  int n, nb, L, H, hkv, max_blocks, num_pages;
   int hg, hpt, rows, mtiles, per_group, S, cap, T, tiles;   // per_group: units of a layout row
   float scale_log2;
 };
@@ -1490,7 +1493,6 @@ int run(bool tree, const void* q, const void* k_tree, const void* v_tree, const 
   p.hkv = kv_heads / batch;
   p.max_blocks = max_blocks;
   p.num_pages = num_pages;
-  p.max_row = layout->max_row;
   p.hg = pl.hg;
   p.hpt = pl.hpt;
   p.rows = pl.rows;
