@@ -5,6 +5,7 @@
 
 #include <cmath>
 #include <cstring>
+#include <memory>
 #include <mutex>
 #include <new>
 #include <string>
@@ -18,6 +19,8 @@ thread_local std::string g_last_error;
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+constexpr size_t kStagedLayoutBytes = size_t(1) << 20;
 }  // namespace
 
 namespace bsa {
@@ -112,22 +115,31 @@ int bsa_build_layout(const bsa_pattern* spec, int n, int B, int layout_heads, in
                        std::string("cudaMalloc: ") + cudaGetErrorString(e));
     }
     char* c = static_cast<char*>(base);
-    e = cudaMemcpy(c, lay->row_ptr.data(), b_rp, cudaMemcpyHostToDevice);
-    if (e == cudaSuccess && !lay->col_idx.empty())
-      e = cudaMemcpy(c + o_ci, lay->col_idx.data(), lay->col_idx.size() * sizeof(int32_t),
-                     cudaMemcpyHostToDevice);
-    if (e == cudaSuccess) e = cudaMemcpy(c + o_or, lay->order.data(), b_or, cudaMemcpyHostToDevice);
-    if (e == cudaSuccess) e = cudaMemcpy(c + o_cp, lay->col_ptr.data(), b_cp, cudaMemcpyHostToDevice);
+    // A small layout goes over in one copy, staged with its cleared status block
+    // (each copy costs about 7 us, whatever its size); a large one array by array.
+    const std::unique_ptr<char[]> stage(total <= kStagedLayoutBytes ? new (std::nothrow) char[total]() : nullptr);
+    auto put = [&](size_t at, const std::vector<int32_t>& v) {
+      if (e != cudaSuccess || v.empty()) return;
+      if (stage) std::memcpy(stage.get() + at, v.data(), v.size() * sizeof(int32_t));
+      else e = cudaMemcpy(c + at, v.data(), v.size() * sizeof(int32_t), cudaMemcpyHostToDevice);
+    };
+    put(0, lay->row_ptr);
+    put(o_ci, lay->col_idx);
+    put(o_or, lay->order);
+    put(o_cp, lay->col_ptr);
+    put(o_ri, lay->row_idx);
+    put(o_sp, lay->seg_ptr);
+    put(o_sg, lay->segs);
+    put(o_wk, lay->work);
+    if (stage) e = cudaMemcpy(c, stage.get(), total, cudaMemcpyHostToDevice);
+    else if (e == cudaSuccess) e = cudaMemset(c + o_st, 0, bsa::kStatusBlockBytes);
     if (e == cudaSuccess && !lay->row_idx.empty())
-      e = cudaMemcpy(c + o_ri, lay->row_idx.data(), lay->row_idx.size() * sizeof(int32_t),
-                     cudaMemcpyHostToDevice);
-    if (e == cudaSuccess && !lay->csr_pos.empty())
-      e = cudaMemcpy(c + o_ps, lay->csr_pos.data(), lay->csr_pos.size() * sizeof(int32_t), cudaMemcpyHostToDevice);
-    if (e == cudaSuccess) e = cudaMemcpy(c + o_sp, lay->seg_ptr.data(), b_sp, cudaMemcpyHostToDevice);
-    if (e == cudaSuccess && !lay->segs.empty())
-      e = cudaMemcpy(c + o_sg, lay->segs.data(), lay->segs.size() * sizeof(int32_t), cudaMemcpyHostToDevice);
-    if (e == cudaSuccess) e = cudaMemcpy(c + o_wk, lay->work.data(), b_wk, cudaMemcpyHostToDevice);
-    if (e == cudaSuccess) e = cudaMemset(c + o_st, 0, bsa::kStatusBlockBytes);
+      e = bsa::fill_csr_pos(reinterpret_cast<const int32_t*>(c), reinterpret_cast<const int32_t*>(c + o_ci),
+                            reinterpret_cast<const int32_t*>(c + o_cp), reinterpret_cast<const int32_t*>(c + o_ri),
+                            lay->nb, layout_heads * lay->nb, int(lay->row_idx.size()),
+                            reinterpret_cast<int32_t*>(c + o_ps));
+    // calls on streams that do not wait for the default stream may come next
+    if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);
     if (e != cudaSuccess) {
       cudaFree(base);
       delete lay;

@@ -39,7 +39,6 @@ struct bsa_layout {
   std::vector<int32_t> work;
   std::vector<int32_t> col_ptr;   // [L*nb + 1]: transposed layout (CSC), per layout head
   std::vector<int32_t> row_idx;   // [nnz]: query blocks keeping each key block, ascending
-  std::vector<int32_t> csr_pos;   // [nnz]: where each entry of the transposed layout stands in col_idx
   std::vector<int32_t> seg_ptr;   // [L + 1]: column segments of layout head h are seg_ptr[h] .. seg_ptr[h+1]
   std::vector<int32_t> segs;      // [3 * segments]: (key block j, first row_idx entry, entries <= kColumnSegment)
   int max_segs = 0;               // most segments of one layout head
@@ -50,7 +49,7 @@ struct bsa_layout {
   const int32_t* d_work = nullptr;   // 16-byte aligned
   const int32_t* d_col_ptr = nullptr;
   const int32_t* d_row_idx = nullptr;
-  const int32_t* d_csr_pos = nullptr;
+  const int32_t* d_csr_pos = nullptr;   // [nnz]: where each entry of the transposed layout stands in col_idx
   const int32_t* d_seg_ptr = nullptr;
   const int32_t* d_segs = nullptr;
   uint32_t* d_status = nullptr;   // bit 0: a device wait ran out
@@ -99,6 +98,11 @@ int launch_dependent(const char* what, F kern, unsigned grid, unsigned threads, 
 
 // Host layout compiler (bsa_layout.cpp).  Fills every host array and max_row, max_segs.
 int compile_layout(const bsa_pattern& spec, int n, int B, int L, bsa_layout* out);
+
+// Enqueues on the legacy default stream the kernel that fills csr_pos from the
+// other arrays of a layout on the current device (bsa_weights_sm100a.cu).
+cudaError_t fill_csr_pos(const int32_t* row_ptr, const int32_t* col_idx, const int32_t* col_ptr, const int32_t* row_idx,
+                         int nb, int rows, int nnz, int32_t* csr_pos);
 
 // Longest run of query blocks one key/value-gradient work item takes from a
 // column of the transposed layout.

@@ -144,7 +144,6 @@ int compile_layout(const bsa_pattern& spec, int n, int B, int L, bsa_layout* out
   // h and key block j, the query blocks whose rows keep j, ascending.
   out->col_ptr.assign(size_t(L) * nb + 1, 0);
   out->row_idx.assign(out->col_idx.size(), 0);
-  out->csr_pos.assign(out->col_idx.size(), 0);
   for (int h = 0; h < L; ++h)
     for (int i = 0; i < nb; ++i) {
       const size_t r = size_t(h) * nb + i;
@@ -157,11 +156,8 @@ int compile_layout(const bsa_pattern& spec, int n, int B, int L, bsa_layout* out
     for (int h = 0; h < L; ++h)
       for (int i = 0; i < nb; ++i) {
         const size_t r = size_t(h) * nb + i;
-        for (int32_t e = out->row_ptr[r]; e < out->row_ptr[r + 1]; ++e) {
-          const int32_t c = fill[size_t(h) * nb + out->col_idx[e]]++;
-          out->row_idx[c] = i;
-          out->csr_pos[c] = e;
-        }
+        for (int32_t e = out->row_ptr[r]; e < out->row_ptr[r + 1]; ++e)
+          out->row_idx[fill[size_t(h) * nb + out->col_idx[e]]++] = i;
       }
   }
 
