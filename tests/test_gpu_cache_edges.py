@@ -339,3 +339,90 @@ def test_calls_that_follow_each_other_unsynchronised(kind, n, B, L, H, G, d, pat
     bsa.bsa_get_status(short.handle)
     lay.close()
     short.close()
+
+
+# ------------------------------------------------------------------ shapes between the others
+
+@pytest.mark.parametrize("B,L,H,G,d", [(64, 1, 24, 1, 64), (128, 1, 20, 2, 128), (64, 16, 16, 1, 64), (128, 10, 10, 1, 64)])
+def test_prompt_weights_of_many_query_heads_a_key_value_head(B, L, H, G, d):
+    """More units a key/value head (12, 10, 16 and 10) than the sum over rows looks up at a time."""
+    n, pat = 900, dict(density=0.4, seed=8)
+    lay = _layout(OL.RANDOM, n, B, L, pat)
+    sets = OL.kept_sets(OL.RANDOM, n, B, L, **pat)
+    q, k, v = (to_device_bf16(x) for x in inputs.qkv_bits(H, G, n, d, seeds=(440, 441, 442)))
+    _, lse = bsa.attention(q, k, v, lay)
+    got = bsa.attention_weights(q, k, lse, lay)
+    torch.cuda.synchronize()
+    bsa.bsa_get_status(lay.handle)
+    qh, kh, lse_h = _np(q), _np(k), _np(lse)
+    want = OC.prompt_weights(qh, kh, lse_h, sets, B, d ** -0.5)
+    # 96 additions in a thread of the first kernel at most, then at most 15 rows of H units
+    _close_w(_np(got), want, _e_p(d ** -0.5, d, qh, kh, lse_h), lse_h, terms=96 + 15 * H)
+    lay.close()
+
+
+@pytest.mark.parametrize("n", [1, 2, 40, 63, 64, 65, 128, 190])
+@pytest.mark.parametrize("B,H,G,d", [(64, 2, 1, 64), (128, 4, 2, 128), (64, 12, 1, 64)])
+def test_steps_over_a_few_tokens(n, B, H, G, d):
+    """Rows of one to four chunks, in clusters of one to four, with a page table that is wider than the layout and
+    weights that begin at an odd place."""
+    batch, wide = 3, -(-n // B) + 3
+    lay = _layout(OL.BAND_GLOBAL, n, B, 1, dict(window=2, global_first=1))
+    sets = OL.kept_sets(OL.BAND_GLOBAL, n, B, 1, window=2, global_first=1)
+    kc, vc, table, th = _paged(batch, G, n, B, d, 450, spare=2)
+    full = torch.full((batch, wide), -9, dtype=torch.int32, device="cuda")
+    full[:, :table.shape[1]] = table
+    at = [n - 1, n // 2, 0]
+    q = to_device_bf16(inputs.normal_bf16_bits((batch * H, d), 451))
+    w0 = torch.rand((batch * G, n + 9), device="cuda")
+    w = w0.clone()
+    o, lse = bsa.decode_weights(q, kc, vc, full, _i32(*at), lay, batch, w[:, 3:3 + n])
+    torch.cuda.synchronize()
+    bsa.bsa_get_status(lay.handle)
+    qh, kh, vh = _np(q), np.nan_to_num(_np(kc)), np.nan_to_num(_np(vc))
+    o_ref, lse_ref = OD.decode_step(qh, kh, vh, th, at, sets, B, d ** -0.5)
+    e_p = _e_p(d ** -0.5, d, qh, kh, lse_ref)
+    _close_lse(_np(lse), lse_ref, e_p)
+    _close_o(_np(o), o_ref, e_p, vh)
+    want = OC.step_weights(qh, kh, th, at, lse_ref, sets, B, d ** -0.5, n)
+    base = _np(w0[:, 3:3 + n])
+    bound = want * (2 * e_p + 2.0 ** -21 + H // G * 2.0 ** -24) + 2.0 ** -24 * (want + base)
+    assert np.all(np.abs(_np(w[:, 3:3 + n]) - base - want) <= bound)
+    w[:, 3:3 + n] = w0[:, 3:3 + n]
+    assert torch.equal(w, w0)
+    lay.close()
+
+
+@pytest.mark.parametrize("op,n,m", [("step", 1000, 2), ("step", 5000, 2), ("step", 3000, 16), ("tree", 1000, 3), ("tree", 3000, 40)])
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_a_query_that_is_not_a_number_stays_alone(op, n, m, what):
+    """One query row of NaN or infinity: every other row of its tile as without it, and, in a step, the weights of
+    the other key/value head too."""
+    lay, q, kt, vt, kc, vc, table, end, run, _ = _zero_case((op, n, 64, m, 64), 460)
+    clean = run()
+    h, t = (m // 2, 0) if op == "step" else (1, m // 2)
+    q[h, t] = what
+    dirty = run()
+    for a, b in zip(clean, dirty):
+        assert np.isfinite(a).all()
+        if op == "step":
+            assert np.isnan(b[h]).all() and np.array_equal(np.delete(a, h, 0), np.delete(b, h, 0))
+        else:
+            assert np.isnan(b[h, t]).all()
+            b[h, t] = a[h, t]
+            assert np.array_equal(a, b)
+    lay.close()
+
+
+@pytest.mark.parametrize("op,n,m", [("step", 1000, 2), ("step", 5000, 2), ("step", 3000, 16)])
+def test_weights_of_a_query_that_is_not_a_number(op, n, m):
+    lay, q, kt, vt, kc, vc, table, end, run, _ = _zero_case((op, n, 64, m, 64), 470)
+    w = torch.zeros((2, n), device="cuda")
+    args = (kc, vc, table, _i32(end - 1), lay, 1)
+    bsa.decode_weights(q[:, 0].contiguous(), *args, w)
+    q[m // 2, 0] = float("nan")                       # of the first key/value head
+    w2 = torch.zeros_like(w)
+    bsa.decode_weights(q[:, 0].contiguous(), *args, w2)
+    torch.cuda.synchronize()
+    assert torch.isnan(w2[0, :end]).all() and torch.equal(w2[1], w[1]) and not torch.any(w2[:, end:])
+    lay.close()
