@@ -426,3 +426,82 @@ def test_weights_of_a_query_that_is_not_a_number(op, n, m):
     torch.cuda.synchronize()
     assert torch.isnan(w2[0, :end]).all() and torch.equal(w2[1], w[1]) and not torch.any(w2[:, end:])
     lay.close()
+
+
+# ------------------------------------------------------------------ captured among other work
+
+@pytest.mark.parametrize("n", [1000, 5000])
+def test_captured_behind_copies_clears_and_other_streams(n):
+    """One graph in which each call follows a copy, a clear, a kernel or another stream's work that writes what it
+    reads, and is followed by one that changes it: replayed, the bits of the same work launched eagerly and waited for."""
+    B, H, G, d, T, budget = 64, 4, 2, 64, 5, n // 3
+    lay = _layout(OL.BAND_GLOBAL, n, B, 1, dict(window=n // B + 1, global_first=0))
+    kc0, vc0, table, _ = _paged(1, G, n, B, d, 480)
+    q0, kt0, vt0 = (to_device_bf16(x) for x in inputs.qkv_bits(H, G, T, d, seeds=(481, 482, 483)))
+    qp, kp, vp = (to_device_bf16(x) for x in inputs.qkv_bits(H, G, n, d, seeds=(484, 485, 486)))
+    _, lse_p = bsa.attention(qp, kp, vp, lay)
+    par0, pos0, len0 = _i32(-1, 0, 0, 1, 3).view(1, T), _i32(n - 20), _i32(n - 19)
+    h = lay.handle
+    ws = [torch.empty(max(16, x), dtype=torch.uint8, device="cuda") for x in (
+        bsa.bsa_attention_weights_workspace_bytes(h, H, G), bsa.bsa_decode_weights_workspace_bytes(h, 1, H, G, d),
+        bsa.bsa_decode_tree_workspace_bytes(h, 1, H, G, T, d), bsa.bsa_evict_workspace_bytes(h, 1, G, budget))]
+
+    def bufs():
+        return dict(q=torch.zeros_like(q0), q1=torch.zeros_like(q0[:, 0]), kt=torch.zeros_like(kt0), vt=torch.zeros_like(vt0),
+                    kc=kc0.clone(), vc=vc0.clone(), par=torch.zeros_like(par0), pos=torch.zeros_like(pos0),
+                    len=torch.zeros_like(len0), w=torch.full((G, n), 3.0, device="cuda"), o=torch.zeros_like(q0),
+                    lse=torch.zeros((H, T), device="cuda"), o1=torch.zeros_like(q0[:, 0]), lse1=torch.zeros(H, device="cuda"),
+                    wo=torch.zeros((G, n), device="cuda"), to=torch.zeros((G, n), dtype=torch.int32, device="cuda"),
+                    lo=torch.zeros_like(len0))
+
+    def work(x, other, wait):
+        main = torch.cuda.current_stream()
+        x["w"].zero_()
+        wait()
+        bsa.attention_weights(qp, kp, lse_p, lay, x["w"], workspace=ws[0])
+        wait()
+        x["q1"].copy_(q0[:, 0])
+        x["pos"].copy_(pos0)
+        wait()
+        bsa.decode_weights(x["q1"], x["kc"], x["vc"], table, x["pos"], lay, 1, x["w"], o=x["o1"], lse=x["lse1"], workspace=ws[1])
+        x["q1"].zero_()
+        x["w"].add_(1.0)
+        wait()
+        # the tree and its inputs on another stream, the cut on this one once both are done
+        other.wait_stream(main)
+        with torch.cuda.stream(other):
+            for a, b in (("q", q0), ("kt", kt0), ("vt", vt0), ("par", par0), ("len", len0)):
+                x[a].copy_(b)
+            wait()
+            bsa.decode_tree(x["q"], x["kt"], x["vt"], x["kc"], x["vc"], table, x["len"], x["par"], lay, o=x["o"], lse=x["lse"],
+                            workspace=ws[2])
+        main.wait_stream(other)
+        wait()
+        bsa.evict(x["kc"], x["vc"], table, x["len"], x["w"], lay, budget, 10, weights_out=x["wo"], tokens_out=x["to"],
+                  lengths_out=x["lo"], workspace=ws[3])
+        x["len"].zero_()
+        x["w"].fill_(-1.0)
+
+    want, got, live = bufs(), bufs(), bufs()
+    other = torch.cuda.Stream()
+    work(want, other, torch.cuda.synchronize)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        work(got, other, lambda: None)
+    for _ in range(3):
+        for name in ("kc", "vc"):
+            got[name].copy_({"kc": kc0, "vc": vc0}[name])
+            live[name].copy_(got[name])
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        work(live, other, lambda: None)
+        torch.cuda.synchronize()
+        for name in want:
+            for x in (got, live):
+                assert torch.equal(x[name].contiguous().view(torch.uint8), want[name].contiguous().view(torch.uint8)), name
+    assert got["lo"].tolist() == [budget] and torch.isfinite(got["wo"]).all()
+    bsa.bsa_get_status(h)
+    del g
+    lay.close()
