@@ -354,7 +354,8 @@ size_t bsa_evict_workspace_bytes(const bsa_layout* layout, int batch, int kv_hea
  * [batch][max_blocks], lengths, lengths_out [batch], tokens, tokens_out int32;
  * weights, weights_out fp32, rows of all four `stride` elements apart.  The
  * layout supplies the device, B, n and the status word (its kept blocks are
- * not read).  Requirements (checked before launch; errors launch nothing):
+ * not read: a block-diagonal one, BAND_GLOBAL with window 0, is the cheapest to
+ * build).  Requirements (checked before launch; errors launch nothing):
  * layout on the current device, n at most 2^30; B in {64, 128}; d in {64, 128};
  * batch, kv_heads, budget, num_pages >= 1; kv_heads a multiple of batch;
  * 0 <= recent <= budget; max_blocks >= the layout's blocks; stride >= n;
