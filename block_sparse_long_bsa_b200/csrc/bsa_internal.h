@@ -100,7 +100,7 @@ int launch_dependent(const char* what, F kern, unsigned grid, unsigned threads, 
 int compile_layout(const bsa_pattern& spec, int n, int B, int L, bsa_layout* out);
 
 // Enqueues on the legacy default stream the kernel that fills csr_pos from the
-// other arrays of a layout on the current device (bsa_weights_sm100a.cu).
+// other arrays of a layout on the current device (bsa_layout_device.cu).
 cudaError_t fill_csr_pos(const int32_t* row_ptr, const int32_t* col_idx, const int32_t* col_ptr, const int32_t* row_idx,
                          int nb, int rows, int nnz, int32_t* csr_pos);
 
