@@ -126,9 +126,9 @@ struct KernelShape {
   static constexpr int kOffBar = kOffV + kVSlots * kTileBytes;
   // barriers: q_full, q_free, k_full[2], v_full[3], s_full[2], p_full[2],
   //           o_done[VS], o_free, drain, never, item_full[8], k_free[KS],
-  //           stage_free[8]
+  //           stage_free[8], empty
   static constexpr int kPend = 8;                            // producer's pending-staging FIFO
-  static constexpr int kNumBars = 2 + kKSlots + kVSlots + 2 + 2 + kODone + 3 + kItemSlots + kKSlots + kPend;
+  static constexpr int kNumBars = 2 + kKSlots + kVSlots + 2 + 2 + kODone + 3 + kItemSlots + kKSlots + kPend + 1;
   static constexpr int kWarpStage = 32 * 128;                // one warp's 32 rows x 64 columns of o
   static_assert(4 * (HD / 64) * kWarpStage == 2 * kTileBytes, "o staging fills two V slots");
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
@@ -268,6 +268,11 @@ __global__ void __launch_bounds__(kThreads, MIN_CTAS)
   const uint32_t bStageFree0 = bKFree0 + 8u * kKSlots;
   auto bStageFree = [&](int e) { return bStageFree0 + 8u * (e % S::kPend); };
   auto parStage = [](int e) { return uint32_t(e / S::kPend) & 1u; };
+  // An item without kept blocks goes through no product, so nothing would keep
+  // the softmax warps, which hand O over at once, from doing so a second time
+  // before the MMA thread has looked: its wait would miss a phase and run
+  // out.  empty completes when the MMA thread takes such an item up.
+  const uint32_t bEmpty = bStageFree0 + 8u * S::kPend;
   // slot k % 8: {valid, row, start, len, h0, kvh, diag_last}
   volatile int* item_ring = reinterpret_cast<volatile int*>(gbase + S::kOffItems);
   auto read_item = [&](int k, Item& it) -> bool {
@@ -316,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, MIN_CTAS)
     for (int s = 0; s < S::kPend; ++s) mbar_init(bStageFree0 + 8u * s, 4);
     for (int s = 0; s < kItemSlots; ++s) mbar_init(bItemFull0 + 8u * s, 1);
     for (int s = 0; s < kKSlots; ++s) mbar_init(bKFree0 + 8u * s, 1);
+    mbar_init(bEmpty, 1);
     *abort_flag = 0;
     fence_barrier_init();
     if (!p.debug_never) {
@@ -487,6 +493,7 @@ __global__ void __launch_bounds__(kThreads, MIN_CTAS)
         if (nch == 0) {
           // keep the O hand-over in step with the softmax warps
           if (k > 0 && !(ok = ctl.wait(bOFree, (k - 1) & 1))) break;
+          mbar_arrive(bEmpty);
           tc_commit(bQFree);
         } else {
           ok = issue_qk(0);
@@ -513,6 +520,7 @@ __global__ void __launch_bounds__(kThreads, MIN_CTAS)
     int s_cnt = 0;                           // chunks seen (global chunk index base)
     bool stage_pending = false;              // this warp's last staging stores not yet released
     int n_staged = 0;                        // items with at least one chunk staged so far
+    int n_empty = 0;                         // items without a chunk so far
     // Once the TMA stores of the previous epilogue have read the staging box,
     // tell the producer (one arrival per warp); deferred so the store drains
     // while this warp already works on the next item.
@@ -709,6 +717,9 @@ __global__ void __launch_bounds__(kThreads, MIN_CTAS)
 #pragma unroll
           for (int w4 = 0; w4 < HD / 8; ++w4) st_global_v4(orow + w4 * 16, z);
         }
+        ok = __all_sync(0xffffffffu, ctl.wait(bEmpty, uint32_t(n_empty) & 1u));
+        if (!ok) break;
+        ++n_empty;
         tc_fence_before();
         mbar_arrive(bOFree);
       }
