@@ -437,13 +437,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- products
     if (lane == 0) {
       bool ok = true;
-      // cursor load: the next non-empty item from ring item k on; the dQ
-      // cursor, the later of the two, hands each slot back once copied
-      auto seek = [&](DqCursor& cu, bool release) {
+      // the next non-empty item from ring item k on; each slot is handed back once copied
+      auto seek = [&](DqCursor& cu) {
         while (ok) {
           if (!(ok = ctl.wait(bar(S::kBItem + cu.k % kRing), uint32_t(cu.k / kRing) & 1u))) break;
           cu.it = read_slot(ring, cu.k);
-          if (release) mbar_arrive(bar(S::kBItemFree + cu.k % kRing));
+          mbar_arrive(bar(S::kBItemFree + cu.k % kRing));
           if (cu.it.last) {
             cu.valid = false;
             return;
@@ -456,13 +455,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         cu.valid = false;
       };
-      auto advance = [&](DqCursor& cu, bool release) {
+      auto advance = [&](DqCursor& cu) {
         ++cu.g;
         if (++cu.c < dq_steps(cu.it)) return;
         cu.c = 0;
         ++cu.xi;
         ++cu.k;
-        seek(cu, release);
+        seek(cu);
       };
       // Every wait for a load (or an accumulator hand-back) is taken before
       // the wait for the row threads that precedes the product, so no
@@ -495,24 +494,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_commit(bar(S::kBDP));
         if (cs.c == dq_steps(cs.it) - 1) tc_commit(bar(S::kBQFree + (cs.xi & 1)));   // last reader of Q, dO
       };
+      // S and dP of a step that was not looked ahead to: a CTA's first one, and
+      // the first one behind items without kept blocks
+      auto start = [&](const DqCursor& cs) -> bool {
+        if (!loads_s(cs) || !ctl.wait(bar(S::kBV), uint32_t(cs.g) & 1u)) return false;
+        issue_s(cs);
+        issue_dp(cs);
+        return true;
+      };
       DqCursor cd{0, 0, 0, 0, {}, false};
-      seek(cd, true);
-      if (cd.valid) {
-        ok = loads_s(cd) && ctl.wait(bar(S::kBV), uint32_t(cd.g) & 1u);
-        if (ok) {
-          issue_s(cd);
-          issue_dp(cd);
-        }
-      }
+      seek(cd);
+      if (cd.valid) ok = start(cd);
       while (ok && cd.valid) {
         DqCursor nx = cd;                      // the next step (same item or the next one)
         {
           ++nx.g;
           if (++nx.c >= dq_steps(nx.it)) {
+            // Only the next item is looked at: the ring holds no more than
+            // eight, and those behind an item without kept blocks may not be
+            // in it before this step's item is done.
             nx.c = 0;
             ++nx.xi;
             ++nx.k;
-            seek(nx, false);
+            if (!(ok = ctl.wait(bar(S::kBItem + nx.k % kRing), uint32_t(nx.k / kRing) & 1u))) break;
+            nx.it = read_slot(ring, nx.k);
+            nx.valid = !nx.it.last && nx.it.nch > 0;
           }
         }
         if (nx.valid && !(ok = loads_s(nx))) break;
@@ -540,7 +546,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (cd.c == dq_steps(cd.it) - 1) tc_commit(bar(S::kBAcc + (cd.xi & 1)));
         }
         if (nx.valid) issue_dp(nx);
-        advance(cd, true);
+        advance(cd);
+        if (cd.valid && !nx.valid) ok = start(cd);
       }
       tc_commit(bar(S::kBDrain));
       wait_drain(bar(S::kBDrain), 0, kDrainNs);

@@ -1,6 +1,7 @@
 """Masks whose query blocks often keep nothing, with many more work items than
 the GPU runs at once: the kernels take up one item without kept blocks after
-the other, and items with some between them.  Against the fp64 oracle.
+the other, and items with some between them.  Against the fp64 oracle;
+gradients with the tolerances of their other parity tests.
 
 Rows of one or a few keys have outputs as large as a value, so o's bound goes
 by its size: P enters the product rounded to bf16, by at most 2^-8 of itself
@@ -15,9 +16,11 @@ torch = pytest.importorskip("torch")
 import block_sparse_long_bsa_b200 as bsa
 from block_sparse_long_bsa_b200 import inputs
 from oracle import attention as OA
+from oracle import backward as BW
 from oracle import layouts as OL
 
-from gpu_common import bf16_half_ulp, default_scale, device_inputs
+from gpu_common import bf16_half_ulp, default_scale, device_inputs, to_device_bf16
+from test_gpu_backward import assert_grad_close
 from test_gpu_cache import _close_lse, _e_p, _np
 
 pytestmark = pytest.mark.gpu
@@ -94,4 +97,24 @@ def test_prompt_weights_with_empty_rows(case):
     rows = torch.isfinite(lse).view(G, -1).sum(1).double()
     # a probability is off by 2e-5 of itself here at most (norms up to 12), a row's sum by no more
     assert torch.equal(w, w2) and torch.all((w.double().sum(1) - rows).abs() <= 3e-5 * rows)
+    lay.close()
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_gradients_with_empty_rows(case):
+    n, B, L, H, G, d, empty, keep = case
+    lay, sets = _layout(case)
+    (qb, kb, vb), (q, k, v) = device_inputs(H, G, n, d, seeds=(500, 501, 502))
+    dob = inputs.normal_bf16_bits((H, n, d), 503)
+    do, scale, runs = to_device_bf16(dob), default_scale(d), []
+    o, lse = bsa.attention(q, k, v, lay)
+    for _ in range(6):
+        runs.append(bsa.attention_backward(q, k, v, o, lse, do, lay))
+        torch.cuda.synchronize()
+        bsa.bsa_get_status(lay.handle)
+    assert all(torch.equal(r[0], runs[0][0]) for r in runs) and torch.all(runs[0][0][torch.isneginf(lse)] == 0)
+    ref = BW.backward_dense(*(inputs.bf16_bits_to_f64(x) for x in (qb, kb, vb, dob)), sets, B, scale)
+    for r in runs:
+        for name, g, want in zip(("dq", "dk", "dv"), r, ref):
+            assert_grad_close(g.cpu().numpy(), want, f"{case} {name}")
     lay.close()
